@@ -73,6 +73,13 @@ _SIGNATURES = {
     "mla_decode_workspace": (_c_size, [_c_int, _c_int, _c_int]),
     "mla_decode_fwd": (_c_int, [_p, _p, _p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
                                 _c_float, _c_int, _p, _c_size, _p]),
+    "mla_kv_append_fp8": (_c_int, [_p, _c_int, _p, _p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _p]),
+    "mla_kv_gather_fp8": (_c_int, [_p, _p, _p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _p]),
+    "mla_fp8_workspace": (_c_size, [_c_int, _c_int]),
+    "mla_decode_fp8_fwd": (_c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
+                                    _c_float, _p, _c_size, _p]),
+    "mla_extend_fp8_fwd": (_c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                    _c_float, _c_float, _p, _c_size, _p]),
 }
 EXPORTED = tuple(_SIGNATURES)
 
@@ -675,3 +682,148 @@ def mla_decode_fwd(q, kv_buffer, o, kv_indptr, kv_indices, kv_last_page_lens, sm
         int(num_kv_splits), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream())
     _check("mla_decode_fwd", rc)
     return o
+
+
+# ---------------------------------------------------------------- 8-bit latent KV cache
+def _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens):
+    """Checks the cache and page table that the 8-bit cache calls share; returns (batch, pages,
+    page_size, the table's length)."""
+    _cuda(kv_cache, FP8, "kv_cache")
+    _cuda(kv_scale, torch.float32, "kv_scale")
+    if kv_cache.dim() != 4 or kv_cache.shape[2] != 1 or kv_cache.shape[3] != MLA_QK_HEAD_DIM \
+            or not kv_cache.is_contiguous():
+        raise ValueError(f"kv_cache must be a contiguous [pages, page_size, 1, {MLA_QK_HEAD_DIM}] tensor")
+    pages, page_size = kv_cache.shape[0], kv_cache.shape[1]
+    if kv_scale.shape != (pages, 1) or not kv_scale.is_contiguous():
+        raise ValueError(f"kv_scale must be a contiguous [{pages}, 1] tensor")
+    batch = kv_last_page_lens.numel()
+    for t, name in ((kv_indptr, "kv_indptr"), (kv_indices, "kv_indices"), (kv_last_page_lens, "kv_last_page_lens")):
+        _cuda(t, torch.int32, name)
+        if t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-D tensor")
+    if kv_indptr.numel() != batch + 1:
+        raise ValueError("kv_indptr must hold one entry more than kv_last_page_lens")
+    return batch, pages, page_size, kv_indices.numel()
+
+
+def _ranges(indptr, name, batch):
+    _cuda(indptr, torch.int32, name)
+    if indptr.shape != (batch + 1,) or not indptr.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {batch + 1} entries")
+
+
+def _call_on(device, name, tensors, *args):
+    """Calls the library on `device`'s current stream; every tensor must lie on that device."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: all tensors must be on one device, got {device} and {t.device}")
+    lib = load_library()
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = getattr(lib, name)(*args, _stream())
+    else:
+        rc = getattr(lib, name)(*args, _stream())
+    _check(name, rc)
+
+
+def mla_kv_append_fp8(kv_new, append_indptr, kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens):
+    """Appends kv_new bf16 [T, 576] (rows append_indptr[b] .. append_indptr[b+1] are the last
+    tokens of sequence b, whose page table counts them in) to the 8-bit latent cache: kv_cache
+    fp8 [pages, page_size, 1, 576] and kv_scale fp32 [pages, 1], both updated in place. A page
+    whose scale grows has its earlier rows re-coded."""
+    batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
+    _cuda(kv_new, torch.bfloat16, "kv_new")
+    ld = _row_major(kv_new, "kv_new")
+    if kv_new.shape[1] != MLA_QK_HEAD_DIM:
+        raise ValueError(f"kv_new must be [T, {MLA_QK_HEAD_DIM}]")
+    T = kv_new.shape[0]
+    if T <= 1:
+        ld = MLA_QK_HEAD_DIM            # the stride of a single row says nothing
+    _ranges(append_indptr, "append_indptr", batch)
+    _call_on(kv_cache.device, "mla_kv_append_fp8",
+             (kv_new, append_indptr, kv_scale, kv_indptr, kv_indices, kv_last_page_lens),
+             _ptr(kv_new), ld, _ptr(append_indptr), _ptr(kv_cache), _ptr(kv_scale), _ptr(kv_indptr), _ptr(kv_indices),
+             _ptr(kv_last_page_lens), batch, T, pages, page_size, n_idx)
+
+
+def mla_kv_gather_fp8(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens, out_indptr, out):
+    """Reads tokens back from the 8-bit latent cache: out bf16 [T, 576] rows out_indptr[b] ..
+    out_indptr[b+1] become the first tokens of sequence b. Returns out."""
+    batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
+    _cuda(out, torch.bfloat16, "out")
+    ld = _row_major(out, "out")
+    if out.shape[1] != MLA_QK_HEAD_DIM:
+        raise ValueError(f"out must be [T, {MLA_QK_HEAD_DIM}]")
+    if out.shape[0] <= 1:
+        ld = MLA_QK_HEAD_DIM
+    _ranges(out_indptr, "out_indptr", batch)
+    _call_on(kv_cache.device, "mla_kv_gather_fp8", (kv_scale, kv_indptr, kv_indices, kv_last_page_lens, out_indptr, out),
+             _ptr(kv_cache), _ptr(kv_scale), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_lens),
+             _ptr(out_indptr), _ptr(out), ld, batch, out.shape[0], pages, page_size, n_idx)
+    return out
+
+
+def mla_fp8_workspace_bytes(num_heads, num_q):
+    """Workspace bytes of mla_decode_fp8_fwd (num_q = the batch) and mla_extend_fp8_fwd."""
+    return load_library().mla_fp8_workspace(num_heads, num_q)
+
+
+def _mla_fp8_attention(name, q, qo_indptr, kv_cache, kv_scale, o, kv_indptr, kv_indices, kv_last_page_lens, sm_scale,
+                       logit_cap, lse, workspace):
+    batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
+    _cuda(q, torch.bfloat16, "q")
+    _cuda(o, torch.bfloat16, "o")
+    if q.dim() != 3 or q.shape[2] != MLA_QK_HEAD_DIM or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous [rows, heads, {MLA_QK_HEAD_DIM}] tensor")
+    rows, heads = q.shape[0], q.shape[1]
+    if o.shape != (rows, heads, MLA_V_HEAD_DIM) or not o.is_contiguous():
+        raise ValueError(f"o must be a contiguous [{rows}, {heads}, {MLA_V_HEAD_DIM}] tensor")
+    if lse is not None:
+        _cuda(lse, torch.float32, "lse")
+        if lse.shape != (rows, heads) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous [{rows}, {heads}] tensor")
+    if qo_indptr is None:
+        if rows != batch:
+            raise ValueError(f"q must hold one row per sequence ({batch}), got {rows}")
+        ranges, sizes = (), (batch, heads)
+    else:
+        _ranges(qo_indptr, "qo_indptr", batch)
+        ranges, sizes = (_ptr(qo_indptr),), (batch, rows, heads)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(MLA_QK_HEAD_DIM)
+    if workspace is None:
+        need = mla_fp8_workspace_bytes(heads, rows)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _cuda(workspace, torch.uint8, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _call_on(kv_cache.device, name,
+             (q, qo_indptr, kv_scale, o, kv_indptr, kv_indices, kv_last_page_lens, lse, workspace),
+             _ptr(q), *ranges, _ptr(kv_cache), _ptr(kv_scale), _ptr(o), _ptr(kv_indptr), _ptr(kv_indices),
+             _ptr(kv_last_page_lens), _ptr(lse), *sizes, pages, page_size, n_idx, float(sm_scale), float(logit_cap),
+             _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return o
+
+
+def mla_decode_fp8_fwd(q, kv_cache, kv_scale, o, kv_indptr, kv_indices, kv_last_page_lens, sm_scale=None,
+                       logit_cap=0.0, lse=None, workspace=None):
+    """MLA decode over the 8-bit latent cache (kv_cache fp8 [pages, page_size, 1, 576], kv_scale
+    fp32 [pages, 1]): o bf16 [B, Hq, 512] from q bf16 [B, Hq, 576], Hq up to 128. sm_scale
+    defaults to 1/sqrt(576); lse (fp32 [B, Hq], optional) receives the log-sum-exp of the
+    scores. Returns o."""
+    return _mla_fp8_attention("mla_decode_fp8_fwd", q, None, kv_cache, kv_scale, o, kv_indptr, kv_indices,
+                              kv_last_page_lens, sm_scale, logit_cap, lse, workspace)
+
+
+def mla_extend_fp8_fwd(q, qo_indptr, kv_cache, kv_scale, o, kv_indptr, kv_indices, kv_last_page_lens, sm_scale=None,
+                       logit_cap=0.0, lse=None, workspace=None):
+    """MLA of several query tokens per sequence over the 8-bit latent cache: rows qo_indptr[b] ..
+    qo_indptr[b+1] of q bf16 [T, Hq, 576] are the last tokens of sequence b, each seeing the
+    tokens up to its own. o bf16 [T, Hq, 512], lse fp32 [T, Hq]; the rest as mla_decode_fp8_fwd.
+    Returns o."""
+    if qo_indptr is None:
+        raise ValueError("qo_indptr is required")
+    return _mla_fp8_attention("mla_extend_fp8_fwd", q, qo_indptr, kv_cache, kv_scale, o, kv_indptr, kv_indices,
+                              kv_last_page_lens, sm_scale, logit_cap, lse, workspace)

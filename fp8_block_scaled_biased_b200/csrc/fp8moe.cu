@@ -23,6 +23,8 @@
 #include "tp_reduce.cuh"
 #include "ep_peer.cuh"
 #include "mla_decode.cuh"
+#include "mla_fp8_cache.cuh"
+#include "mla_fp8_attn.cuh"
 
 static_assert(fp8moe::kMoeBlockRows == fp8moe::kBM, "sorted blocks are GEMM tiles");
 
@@ -1123,6 +1125,159 @@ int mla_decode_fwd(const uint16_t* q, const uint16_t* kv_buffer, uint16_t* o, co
     return check_launch("mla_decode_fwd (combine)");
   }
   return FP8MOE_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ the 8-bit latent cache
+namespace {
+
+// The checks that the cache calls share; fills `t`. Row numbers of the cache and token
+// positions are int32 in the kernels.
+int cache_table(const char* name, const void* kv_cache, const void* kv_scale, const int32_t* kv_indptr,
+                const int32_t* kv_indices, const int32_t* kv_last_page_lens, int batch, int num_pages, int page_size,
+                int num_indices, PageTable* t) {
+  if (batch < 0 || num_pages < 0 || num_indices < 0) return fail(FP8MOE_EINVAL, "%s: negative size", name);
+  if (page_size < 1) return fail(FP8MOE_EINVAL, "%s: page_size must be >= 1", name);
+  if (batch > (1 << 20)) return fail(FP8MOE_EUNSUPPORTED, "%s: batch above 2^20", name);
+  if (batch > 0 && (!kv_indptr || !kv_last_page_lens)) return fail(FP8MOE_EINVAL, "%s: null pointer argument", name);
+  if (num_indices > 0 && (!kv_indices || !kv_cache || !kv_scale || num_pages < 1))
+    return fail(FP8MOE_EINVAL, "%s: page indices given without a cache", name);
+  if (kv_cache && !aligned16(kv_cache)) return fail(FP8MOE_EINVAL, "%s: kv_cache must be 16-byte aligned", name);
+  if (static_cast<long long>(num_pages) * page_size >= (1ll << 31))
+    return fail(FP8MOE_EUNSUPPORTED, "%s: num_pages x page_size must stay below 2^31", name);
+  if (static_cast<long long>(num_indices) * page_size >= (1ll << 31))
+    return fail(FP8MOE_EUNSUPPORTED, "%s: num_indices x page_size must stay below 2^31", name);
+  *t = PageTable{kv_indptr, kv_indices, kv_last_page_lens, batch, num_pages, page_size, num_indices};
+  return FP8MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_kv_append_fp8(const uint16_t* kv_new, int ld_new, const int32_t* append_indptr, uint8_t* kv_cache,
+                      float* kv_scale, const int32_t* kv_indptr, const int32_t* kv_indices,
+                      const int32_t* kv_last_page_lens, int batch, int num_tokens, int num_pages, int page_size,
+                      int num_indices, void* stream) {
+  const char* name = "mla_kv_append_fp8";
+  AppendArgs a{};
+  if (int rc = cache_table(name, kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens, batch, num_pages,
+                           page_size, num_indices, &a.table))
+    return rc;
+  if (num_tokens < 0) return fail(FP8MOE_EINVAL, "%s: negative size", name);
+  if (num_tokens > (1 << 30)) return fail(FP8MOE_EUNSUPPORTED, "%s: more than 2^30 tokens", name);
+  if (ld_new < kLatDk || ld_new % 8) return fail(FP8MOE_EINVAL, "%s: ld_new must be a multiple of 8, at least 576", name);
+  if (batch == 0 || num_tokens == 0) return FP8MOE_OK;
+  if (!kv_new || !append_indptr) return fail(FP8MOE_EINVAL, "%s: null pointer argument", name);
+  if (!aligned16(kv_new)) return fail(FP8MOE_EINVAL, "%s: kv_new must be 16-byte aligned", name);
+  if (!kv_cache || !kv_scale) return fail(FP8MOE_EINVAL, "%s: null cache", name);
+  int sms = 0;
+  if (int rc = device_setup(&sms)) return rc;
+  a.kv_new = reinterpret_cast<const __nv_bfloat16*>(kv_new);
+  a.ld = ld_new;
+  a.append_indptr = append_indptr;
+  a.cache = kv_cache;
+  a.scale = kv_scale;
+  a.T = num_tokens;
+  // threads for at most four 16-byte pieces each of a full page's rows, or of all new rows
+  const long long pieces = std::min<long long>(page_size, num_tokens) * kLatVec;
+  const int threads = static_cast<int>(std::min(512ll, std::max(96ll, (pieces / 4 + 31) / 32 * 32)));
+  const unsigned ctas = static_cast<unsigned>(num_tokens / page_size + 2 * batch);
+  mla_kv_append_kernel<<<ctas, threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return check_launch(name);
+}
+
+int mla_kv_gather_fp8(const uint8_t* kv_cache, const float* kv_scale, const int32_t* kv_indptr,
+                      const int32_t* kv_indices, const int32_t* kv_last_page_lens, const int32_t* out_indptr,
+                      uint16_t* out, int ld_out, int batch, int num_rows, int num_pages, int page_size,
+                      int num_indices, void* stream) {
+  const char* name = "mla_kv_gather_fp8";
+  GatherArgs a{};
+  if (int rc = cache_table(name, kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens, batch, num_pages,
+                           page_size, num_indices, &a.table))
+    return rc;
+  if (num_rows < 0) return fail(FP8MOE_EINVAL, "%s: negative size", name);
+  if (num_rows > (1 << 30)) return fail(FP8MOE_EUNSUPPORTED, "%s: more than 2^30 rows", name);
+  if (ld_out < kLatDk || ld_out % 8) return fail(FP8MOE_EINVAL, "%s: ld_out must be a multiple of 8, at least 576", name);
+  if (batch == 0 || num_rows == 0) return FP8MOE_OK;
+  if (!out || !out_indptr) return fail(FP8MOE_EINVAL, "%s: null pointer argument", name);
+  if (!aligned16(out)) return fail(FP8MOE_EINVAL, "%s: out must be 16-byte aligned", name);
+  int sms = 0;
+  if (int rc = device_setup(&sms)) return rc;
+  a.cache = kv_cache;
+  a.scale = kv_scale;
+  a.out_indptr = out_indptr;
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.ld = ld_out;
+  a.T = num_rows;
+  mla_kv_gather_kernel<<<(num_rows + kGatherRows - 1) / kGatherRows, kGatherThreads, 0,
+                         static_cast<cudaStream_t>(stream)>>>(a);
+  return check_launch(name);
+}
+
+size_t mla_fp8_workspace(int num_heads, int num_q) {
+  (void)num_heads;
+  (void)num_q;
+  return 0;
+}
+
+static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t* qo_indptr, const uint8_t* kv_cache,
+                             const float* kv_scale, uint16_t* o, const int32_t* kv_indptr, const int32_t* kv_indices,
+                             const int32_t* kv_last_page_lens, float* lse, int batch, int num_q, int num_heads,
+                             int num_pages, int page_size, int num_indices, float sm_scale, float logit_cap,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  LatAttnArgs a{};
+  if (int rc = cache_table(name, kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens, batch, num_pages,
+                           page_size, num_indices, &a.table))
+    return rc;
+  if (num_q < 0) return fail(FP8MOE_EINVAL, "%s: negative size", name);
+  if (num_heads < 1 || num_heads > 128)
+    return fail(FP8MOE_EUNSUPPORTED, "%s: num_heads must be 1 to 128 (got %d)", name, num_heads);
+  if (num_q > (1 << 22)) return fail(FP8MOE_EUNSUPPORTED, "%s: more than 2^22 query tokens", name);
+  if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return fail(FP8MOE_EINVAL, "%s: sm_scale must be finite and > 0", name);
+  if (!(logit_cap >= 0.0f) || !std::isfinite(logit_cap))
+    return fail(FP8MOE_EINVAL, "%s: logit_cap must be finite and >= 0", name);
+  if (batch == 0 || num_q == 0) return FP8MOE_OK;
+  if (!q || !o) return fail(FP8MOE_EINVAL, "%s: null pointer argument", name);
+  if (!aligned16(q) || !aligned16(o)) return fail(FP8MOE_EINVAL, "%s: q and o must be 16-byte aligned", name);
+  const size_t need = mla_fp8_workspace(num_heads, num_q);
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(FP8MOE_EWORKSPACE, "%s: workspace of %zu bytes (16-byte aligned) needed", name, need);
+  int sms = 0;
+  if (int rc = device_setup(&sms)) return rc;
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.qo_indptr = qo_indptr;
+  a.cache = kv_cache;
+  a.scale = kv_scale;
+  a.o = reinterpret_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.num_q = num_q;
+  a.Hq = num_heads;
+  a.sm_scale = sm_scale;
+  a.logit_cap = logit_cap;
+  mla_fp8_simple_kernel<<<dim3(num_q, (num_heads + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return check_launch(name);
+}
+
+int mla_decode_fp8_fwd(const uint16_t* q, const uint8_t* kv_cache, const float* kv_scale, uint16_t* o,
+                       const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* kv_last_page_lens,
+                       float* lse, int batch, int num_heads, int num_pages, int page_size, int num_indices,
+                       float sm_scale, float logit_cap, void* workspace, size_t workspace_bytes, void* stream) {
+  return mla_fp8_attention("mla_decode_fp8_fwd", q, nullptr, kv_cache, kv_scale, o, kv_indptr, kv_indices,
+                           kv_last_page_lens, lse, batch, batch, num_heads, num_pages, page_size, num_indices, sm_scale,
+                           logit_cap, workspace, workspace_bytes, stream);
+}
+
+int mla_extend_fp8_fwd(const uint16_t* q, const int32_t* qo_indptr, const uint8_t* kv_cache, const float* kv_scale,
+                       uint16_t* o, const int32_t* kv_indptr, const int32_t* kv_indices,
+                       const int32_t* kv_last_page_lens, float* lse, int batch, int num_q, int num_heads,
+                       int num_pages, int page_size, int num_indices, float sm_scale, float logit_cap,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (batch > 0 && num_q > 0 && !qo_indptr) return fail(FP8MOE_EINVAL, "mla_extend_fp8_fwd: null qo_indptr");
+  return mla_fp8_attention("mla_extend_fp8_fwd", q, qo_indptr, kv_cache, kv_scale, o, kv_indptr, kv_indices,
+                           kv_last_page_lens, lse, batch, num_q, num_heads, num_pages, page_size, num_indices, sm_scale,
+                           logit_cap, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,278 @@
+// The 8-bit paged latent KV cache: appending tokens to it and reading them back.
+//
+// The cache holds e4m3 codes [pages, page_size, 576] with one fp32 scale per page (a page
+// is the block of tokens that shares a scale; MLA has one KV head); a value is code * scale.
+// The scale is the smallest power of two s with amax <= 448 s, amax over the page's finite
+// entries, so dividing by it is exact and a page whose scale grows by 2^k only has 2^k
+// taken off its codes' exponents: they stay exact down to e4m3's subnormals, where they are
+// rounded once more. 448 = 1.75 * 2^8 makes the scale's exponent that of amax minus 8, plus
+// one if amax's significand exceeds 1.75.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace fp8moe {
+
+constexpr int kLatDk = 576;                  // entries of a cache row (512 latent + 64 rotary)
+constexpr int kLatVec = kLatDk / 8;          // 16-byte pieces of a bf16 row
+constexpr int kScaleMinExp = -110;           // keeps 1 / scale and products with it normal fp32
+
+// The page table of a batch, and the buffer it points into.
+struct PageTable {
+  const int32_t* indptr;         // [B + 1]
+  const int32_t* indices;        // [num_indices]
+  const int32_t* last_lens;      // [B]
+  int B, num_pages, page_size, num_indices;
+};
+
+// First page-table entry and token count of sequence b; false (and flagged) if the table's
+// entries for it are out of range. An empty sequence is a valid one of 0 tokens.
+__device__ __forceinline__ bool sequence_extent(const PageTable& t, int b, int& first, int& len) {
+  const int lo = __ldg(t.indptr + b), hi = __ldg(t.indptr + b + 1);
+  first = lo;
+  len = 0;
+  if (lo < 0 || hi < lo || hi > t.num_indices) {
+    raise_device_error(FP8MOE_DEVERR_PAGE);
+    return false;
+  }
+  if (hi == lo) return true;
+  const int last = __ldg(t.last_lens + b);
+  if (last < 1 || last > t.page_size) {
+    raise_device_error(FP8MOE_DEVERR_PAGE);
+    return false;
+  }
+  len = (hi - lo - 1) * t.page_size + last;
+  return true;
+}
+
+// The page at entry `at` of the table (already known to be below num_indices); -1 and flagged
+// if it lies outside the buffer.
+__device__ __forceinline__ int table_page(const PageTable& t, int at) {
+  const int page = __ldg(t.indices + at);
+  if (page < 0 || page >= t.num_pages) {
+    raise_device_error(FP8MOE_DEVERR_PAGE);
+    return -1;
+  }
+  return page;
+}
+
+// Four e4m3 codes <-> fp32.
+__device__ __forceinline__ float4 e4m3x4_to_float(uint32_t codes) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return make_float4(x.x, x.y, y.x, y.y);
+}
+__device__ __forceinline__ uint32_t float_to_e4m3x4(float a, float b, float c, float d) {
+  return static_cast<uint32_t>(cvt_e4m3x2(a, b)) | (static_cast<uint32_t>(cvt_e4m3x2(c, d)) << 16);
+}
+__device__ __forceinline__ float2 bf16x2_to_float(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// ---------------------------------------------------------------- append
+struct AppendArgs {
+  const __nv_bfloat16* kv_new;   // [T, 576], row stride ld
+  long long ld;
+  const int32_t* append_indptr;  // [B + 1]
+  uint8_t* cache;
+  float* scale;                  // [num_pages]
+  PageTable table;
+  int T;
+};
+
+constexpr int kAppendHeld = 9;   // 16-byte pieces a thread keeps in registers between the passes
+
+// Two bf16 magnitudes' bit patterns, non-finite ones as 0 (their order is that of the values).
+__device__ __forceinline__ uint32_t finite_magnitudes(uint32_t v) {
+  v &= 0x7fff7fffu;
+  return v & ~__vcmpgeu2(v, 0x7f807f80u);
+}
+
+// One CTA per (sequence, page written): the largest magnitude of the page's new rows, the page's
+// scale, the codes. Sequence b owns the CTAs from floor(append_indptr[b] / page_size) + 2b on:
+// its n tokens touch at most floor(n / page_size) + 2 pages, and the floors leave room for that.
+__global__ void __launch_bounds__(512) mla_kv_append_kernel(const AppendArgs a) {
+  __shared__ uint32_t warp_max[16];
+  const int tid = threadIdx.x, nthreads = blockDim.x;
+  const int ps = a.table.page_size;
+  int before = 0;                                            // sequences whose CTAs start at or before this one
+  for (int b0 = 0; b0 < a.table.B; b0 += nthreads) {
+    const int b = b0 + tid;
+    const bool in = b < a.table.B && __ldg(a.append_indptr + b) / ps + 2ll * b <= blockIdx.x;
+    const int n = __syncthreads_count(in);
+    before += n;
+    if (n < nthreads) break;
+  }
+  if (before == 0) return;
+  const int b = before - 1;
+  const int lo = __ldg(a.append_indptr + b), hi = __ldg(a.append_indptr + b + 1);
+  if (lo < 0 || hi < lo || hi > a.T) {
+    if (tid == 0) raise_device_error(FP8MOE_DEVERR_PAGE);
+    return;
+  }
+  if (hi == lo) return;
+  int first, len;
+  if (!sequence_extent(a.table, b, first, len)) return;
+  const int n = hi - lo, start = len - n;
+  if (start < 0) {
+    if (tid == 0) raise_device_error(FP8MOE_DEVERR_PAGE);
+    return;
+  }
+  const long long j = start / ps + (static_cast<long long>(blockIdx.x) - (lo / ps + 2ll * b));
+  if (j > (len - 1) / ps) return;
+  const int page = table_page(a.table, first + static_cast<int>(j));
+  if (page < 0) return;
+  const long long page_tok = j * ps;                         // first token position of the page
+  const int slot0 = static_cast<int>(max(0ll, start - page_tok));
+  const int rows = static_cast<int>(min(static_cast<long long>(ps), len - page_tok)) - slot0;
+  const __nv_bfloat16* src = a.kv_new + (lo + (page_tok + slot0 - start)) * a.ld;
+  const long long nvec = static_cast<long long>(rows) * kLatVec;
+  auto load = [&](long long v) {
+    const long long r = v / kLatVec;
+    return __ldg(reinterpret_cast<const uint4*>(src + r * a.ld + (v - r * kLatVec) * 8));
+  };
+
+  const float old = slot0 > 0 ? a.scale[page] : 0.0f;        // a page written from its first slot starts afresh
+  uint4 held[kAppendHeld];
+  uint32_t mx = 0;
+  auto take = [&](const uint4& x) {
+    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(finite_magnitudes(x.x), finite_magnitudes(x.y)),
+                               __vmaxu2(finite_magnitudes(x.z), finite_magnitudes(x.w))));
+  };
+#pragma unroll
+  for (int i = 0; i < kAppendHeld; ++i) {
+    const long long v = tid + static_cast<long long>(i) * nthreads;
+    held[i] = v < nvec ? load(v) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kAppendHeld; ++i) take(held[i]);
+  for (long long v = tid + static_cast<long long>(kAppendHeld) * nthreads; v < nvec; v += nthreads) take(load(v));
+  mx = max(mx & 0xffffu, mx >> 16);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if ((tid & 31) == 0) warp_max[tid >> 5] = mx;
+  __syncthreads();
+  for (int w = 0; w < nthreads / 32; ++w) mx = max(mx, warp_max[w]);
+
+  float s = 0.0f;
+  if (mx != 0) {
+    const int ex = max(kScaleMinExp, static_cast<int>(mx >> 7) - 135 + ((mx & 0x7fu) > 96u ? 1 : 0));
+    s = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+  }
+  s = fmaxf(s, old);
+  if (tid == 0) a.scale[page] = s;                           // every thread read `old` before the barrier
+  const float inv = s > 0.0f ? 1.0f / s : 1.0f;
+  uint8_t* page_codes = a.cache + static_cast<size_t>(page) * ps * kLatDk;
+  uint8_t* dst = page_codes + static_cast<size_t>(slot0) * kLatDk;
+  auto store = [&](long long v, const uint4& x) {
+    const float2 f0 = bf16x2_to_float(x.x), f1 = bf16x2_to_float(x.y), f2 = bf16x2_to_float(x.z),
+                 f3 = bf16x2_to_float(x.w);
+    *reinterpret_cast<uint2*>(dst + v * 8) = make_uint2(float_to_e4m3x4(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv),
+                                                        float_to_e4m3x4(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv));
+  };
+#pragma unroll
+  for (int i = 0; i < kAppendHeld; ++i) {
+    const long long v = tid + static_cast<long long>(i) * nthreads;
+    if (v < nvec) store(v, held[i]);
+  }
+  for (long long v = tid + static_cast<long long>(kAppendHeld) * nthreads; v < nvec; v += nthreads) store(v, load(v));
+
+  if (slot0 > 0 && old > 0.0f && s > old) {                  // the rows that were there, in the larger scale
+    const float ratio = old / s;
+    uint4* codes = reinterpret_cast<uint4*>(page_codes);
+    for (long long v = tid; v < static_cast<long long>(slot0) * (kLatDk / 16); v += nthreads) {
+      uint4 x = codes[v];
+      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = e4m3x4_to_float(w[i]);
+        w[i] = float_to_e4m3x4(f.x * ratio, f.y * ratio, f.z * ratio, f.w * ratio);
+      }
+      codes[v] = x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- gather
+struct GatherArgs {
+  const uint8_t* cache;
+  const float* scale;
+  PageTable table;
+  const int32_t* out_indptr;     // [B + 1]
+  __nv_bfloat16* out;            // [T, 576], row stride ld
+  long long ld;
+  int T;
+};
+
+constexpr int kGatherRows = 32;
+constexpr int kGatherThreads = 256;
+
+// A CTA reads back 32 output rows: their cache rows first (a thread each), then 16 codes at a
+// time (one 16-byte load, two 16-byte stores).
+__global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const GatherArgs a) {
+  __shared__ long long row_at[kGatherRows];                  // cache row, or -1
+  __shared__ float row_scale[kGatherRows];
+  const int tid = threadIdx.x;
+  const int t0 = blockIdx.x * kGatherRows;
+  int before = 0;                                            // sequences that start at or before row t0
+  for (int b0 = 0; b0 < a.table.B; b0 += kGatherThreads) {
+    const int b = b0 + tid;
+    const int n = __syncthreads_count(b < a.table.B && __ldg(a.out_indptr + b) <= t0);
+    before += n;
+    if (n < kGatherThreads) break;
+  }
+  if (tid < kGatherRows) {
+    const int t = t0 + tid;
+    long long at = -1;
+    float sc = 0.0f;
+    int b = max(before - 1, 0);
+    while (b < a.table.B && __ldg(a.out_indptr + b + 1) <= t) ++b;
+    if (t < a.T && b < a.table.B) {
+      const int lo = __ldg(a.out_indptr + b);
+      int first, len;
+      if (t >= lo && sequence_extent(a.table, b, first, len)) {
+        const int i = t - lo;
+        if (lo < 0 || i >= len) {
+          raise_device_error(FP8MOE_DEVERR_PAGE);
+        } else {
+          const int page = table_page(a.table, first + i / a.table.page_size);
+          if (page >= 0) {
+            at = static_cast<long long>(page) * a.table.page_size + i % a.table.page_size;
+            sc = __ldg(a.scale + page);
+          }
+        }
+      }
+    }
+    row_at[tid] = at;
+    row_scale[tid] = sc;
+  }
+  __syncthreads();
+  constexpr int kPieces = kLatDk / 16;
+#pragma unroll
+  for (int v = tid; v < kGatherRows * kPieces; v += kGatherThreads) {
+    const int r = v / kPieces, c = v - r * kPieces;
+    const long long at = row_at[r];
+    if (at < 0) continue;
+    const float s = row_scale[r];
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.cache + at * kLatDk) + c);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    __align__(16) __nv_bfloat162 y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = e4m3x4_to_float(w[i]);
+      y[2 * i] = __floats2bfloat162_rn(f.x * s, f.y * s);
+      y[2 * i + 1] = __floats2bfloat162_rn(f.z * s, f.w * s);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(a.out + (t0 + r) * a.ld) + 2 * c;
+    dst[0] = *reinterpret_cast<const uint4*>(&y[0]);
+    dst[1] = *reinterpret_cast<const uint4*>(&y[4]);
+  }
+}
+
+}  // namespace fp8moe

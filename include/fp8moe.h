@@ -60,7 +60,8 @@ enum fp8moe_device_error {
   FP8MOE_DEVERR_PAIR_ID = 4u,     /* a sorted pair id outside [0, T*topk] was met */
   FP8MOE_DEVERR_NUM_VALID = 8u,   /* num_valid_ids above capacity or not a multiple of block_m */
   FP8MOE_DEVERR_BLOCK_ORDER = 16u, /* sorted_expert_ids decreases somewhere: not a moe_align_sort result */
-  FP8MOE_DEVERR_PAGE = 32u         /* MLA decode: a page-table entry outside its range (see mla_decode_fwd) */
+  FP8MOE_DEVERR_PAGE = 32u         /* MLA: a page-table entry outside its range (see mla_decode_fwd), or a token range
+                                      that does not fit its sequence (the 8-bit latent cache's calls) */
 };
 
 /* Message describing the calling thread's most recent failure ("" if none). */
@@ -611,6 +612,102 @@ int mla_decode_fwd(const uint16_t* q, const uint16_t* kv_buffer, uint16_t* o,
                    int num_indices, float sm_scale, float logit_cap,
                    int num_kv_splits, void* workspace, size_t workspace_bytes,
                    void* stream);
+
+/* ---------------------------------------------------------------- 8-bit latent KV cache
+ * MLA's latent cache held in e4m3 with one scale per page, and the attention over it:
+ * the FP8 form of the section's paged KV buffer (half the bytes of a decode step, twice
+ * the context in the same memory).
+ *
+ *   kv_cache     fp8 [num_pages, page_size, 1, 576], contiguous, 16-byte aligned; each row
+ *                is a token's key, its first 512 entries are its value
+ *   kv_scale     fp32 [num_pages, 1]: value = code * scale, one scale per block of tokens
+ *                (a page) and KV head. mla_kv_append_fp8 writes powers of two: the smallest
+ *                s >= 2^-110 with amax <= 448 s, amax over the page's finite entries, 0 for
+ *                a page whose finite entries are all zero. The attention and gather calls
+ *                take any finite scale >= 0.
+ *   kv_indptr, kv_indices, kv_last_page_lens: the page table, as for mla_decode_fwd.
+ *                Sequence b holds L_b = (pages - 1) * page_size + kv_last_page_lens[b] tokens
+ *                (0 without a page). Any page_size >= 1.
+ * Limits of all four calls: batch <= 2^20; num_pages * page_size and num_indices *
+ * page_size below 2^31. A page-table entry, or an append, query or output range, that is
+ * out of range is neither read nor written through: the device error word gets
+ * FP8MOE_DEVERR_PAGE and that sequence's output is unspecified. All are deterministic.
+ */
+
+/*
+ * Appends new tokens' rows. The page table describes the sequences with the new tokens
+ * counted in: sequence b's new rows kv_new[append_indptr[b] .. append_indptr[b + 1]) are its
+ * last n_b tokens, at positions L_b - n_b .. L_b - 1.
+ *   kv_new         bf16 [num_tokens, 576], row stride ld_new (a multiple of 8), 16-byte aligned
+ *   append_indptr  int32 [batch + 1], non-decreasing within [0, num_tokens]; n_b <= L_b
+ * For every page written: old = its scale, or 0 if its first slot is written now (a page
+ * taken over from an earlier owner starts afresh); scale = max(old, the scale of the new
+ * rows); if that exceeds old, the rows the page already held get the codes
+ * e4m3(code * old / scale); new rows get e4m3(x / scale). Rounding is to nearest even;
+ * infinities become +-448, NaN stays NaN. Rows of a page behind the last token, and pages
+ * that no new token falls into, are left as they are.
+ * A page must not be written for two sequences in one call, nor read by work that is not
+ * ordered with this call: its codes and its scale change together.
+ */
+int mla_kv_append_fp8(const uint16_t* kv_new, int ld_new, const int32_t* append_indptr,
+                      uint8_t* kv_cache, float* kv_scale, const int32_t* kv_indptr,
+                      const int32_t* kv_indices, const int32_t* kv_last_page_lens,
+                      int batch, int num_tokens, int num_pages, int page_size,
+                      int num_indices, void* stream);
+
+/*
+ * Reads tokens back in bf16 (a cached prefix for the up-projection of a prompt's keys and
+ * values): out[out_indptr[b] + i] = bf16(code * scale) of token i of sequence b, for the
+ * first out_indptr[b + 1] - out_indptr[b] tokens (at most L_b) of each.
+ *   out_indptr  int32 [batch + 1], non-decreasing within [0, num_rows]
+ *   out         bf16 [num_rows, 576], row stride ld_out (a multiple of 8), 16-byte aligned;
+ *               rows outside the ranges are left as they are
+ */
+int mla_kv_gather_fp8(const uint8_t* kv_cache, const float* kv_scale,
+                      const int32_t* kv_indptr, const int32_t* kv_indices,
+                      const int32_t* kv_last_page_lens, const int32_t* out_indptr,
+                      uint16_t* out, int ld_out, int batch, int num_rows, int num_pages,
+                      int page_size, int num_indices, void* stream);
+
+/*
+ * mla_decode_fwd over the 8-bit cache: one query token per sequence.
+ *   q    bf16 [batch, num_heads, 576], contiguous, 16-byte aligned
+ *   o    bf16 [batch, num_heads, 512], contiguous, 16-byte aligned (output)
+ *   lse  fp32 [batch, num_heads] or NULL: ln(sum_j exp(s_j)) (output)
+ * num_heads is 1 to 128; sm_scale and logit_cap as for mla_decode_fwd. A sequence without
+ * a token gets o = 0 and lse = -inf.
+ *   workspace  mla_fp8_workspace(num_heads, batch) bytes, 16-byte aligned; it needs no
+ *              initialisation and keeps nothing between calls. Calls that may overlap on
+ *              the GPU (other streams, other captured graphs) need one each.
+ * No query is rounded: a bf16 entry is the sum of two e4m3 codes (below 2^-14 of its row's
+ * largest magnitude: to 2^-22 of that). The softmax weights that multiply the values are
+ * rounded to the sum of three e4m3 codes; the sum that divides them, and lse, are not.
+ * An infinite query entry counts as NaN.
+ */
+size_t mla_fp8_workspace(int num_heads, int num_q);
+int mla_decode_fp8_fwd(const uint16_t* q, const uint8_t* kv_cache, const float* kv_scale,
+                       uint16_t* o, const int32_t* kv_indptr, const int32_t* kv_indices,
+                       const int32_t* kv_last_page_lens, float* lse, int batch,
+                       int num_heads, int num_pages, int page_size, int num_indices,
+                       float sm_scale, float logit_cap, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * The same for several query tokens per sequence, causal from the end (drafted tokens
+ * being checked, a prompt's chunk behind its cached prefix): sequence b's queries are rows
+ * qo_indptr[b] .. qo_indptr[b + 1) of q, the last n_b of its L_b tokens, and query i sees
+ * its first L_b - n_b + i + 1 tokens (none: o = 0, lse = -inf).
+ *   q, o, lse  as above with num_q rows; rows outside every range are left as they are
+ *   qo_indptr  int32 [batch + 1], non-decreasing within [0, num_q]
+ *   workspace  mla_fp8_workspace(num_heads, num_q) bytes
+ * num_q <= 2^22.
+ */
+int mla_extend_fp8_fwd(const uint16_t* q, const int32_t* qo_indptr, const uint8_t* kv_cache,
+                       const float* kv_scale, uint16_t* o, const int32_t* kv_indptr,
+                       const int32_t* kv_indices, const int32_t* kv_last_page_lens,
+                       float* lse, int batch, int num_q, int num_heads, int num_pages,
+                       int page_size, int num_indices, float sm_scale, float logit_cap,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,564 @@
+"""GPU parity of the 8-bit latent cache (append, gather) and the attention over it, against the oracle.
+
+Append and gather are exact: codes, scales and bf16 values must match bit for bit.
+
+Attention, from the kernel's arithmetic. With S = sm_scale * max_j <|q|, |k_j|>:
+  * a query entry is split into two e4m3 codes, off by at most 2^-22 of its row's largest
+    magnitude; products of codes are exact, and their fp32 sums of 18 matrix steps (each a
+    truncation, 2^-23) and a few more roundings are off by less than 2^-18 S. A row's
+    largest magnitude is below 16 times its mean here, so the split adds less than
+    16 * 2^-22 S. Score error: below 2^-17 S; with the fp32 exponent's rounding (2^-22 of
+    the argument, itself within 2 S) below 2^-17 (1 + S);
+  * so a softmax weight and its normaliser are each off by 2^-17 (1 + S), together
+    2^-16 (1 + S) relatively;
+  * a weight times its page's scale is the sum of three e4m3 codes: 2^-12 relatively, or
+    2^-25 of the running largest one: at most 2^-24 L of the result's magnitude in all
+    (the largest weight is at least 1/L of the sum when the values are of one size; the
+    tests with pages of very different scales have L <= 512 and large codes of their own);
+  * fp32 sums of L/32 steps: L * 2^-28;
+  * the bf16 output: half a step, 2^-8 relatively.
+|o - o_ref| <= (2^-16 (1 + S) + 2^-12 + 2^-23 L) * sum_j p_j |v_j| + 2^-8 |o_ref| + 1e-30,
+|lse - lse_ref| <= 2^-17 (1 + S) + 2^-21 (1 + |lse_ref|).
+"""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from oracle import mla_fp8_oracle as M8
+from oracle.fp8moe_oracle import e4m3_encode
+from fp8_block_scaled_biased_b200 import binding as B
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device"),
+              pytest.mark.filterwarnings("ignore")]
+
+DEV = "cuda"
+
+
+@pytest.fixture(autouse=True)
+def _device_status_clean():
+    yield
+    assert B.device_status() == 0
+
+
+class Batch:
+    """A cache (CPU codes and scales), a page table with shuffled pages, and their device copies."""
+
+    def __init__(self, lens, ps, seed=0, spare=2, scale_exp=(-6, -5), poison=True, codes=None):
+        g = torch.Generator().manual_seed(seed)
+        self.g, self.ps, self.lens = g, ps, list(lens)
+        counts = [-(-n // ps) for n in self.lens]
+        n = sum(counts) + spare
+        self.codes = e4m3_encode(torch.randn(n, ps, 1, 576, generator=g) * 40) if codes is None else codes(n, ps, g)
+        self.scales = torch.exp2(torch.randint(scale_exp[0], scale_exp[1] + 1, (n, 1), generator=g).float())
+        self.indptr = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32)
+        self.indices = torch.randperm(n, generator=g)[:sum(counts)].to(torch.int32)
+        self.last = torch.tensor([L - (c - 1) * ps if c else 0 for L, c in zip(self.lens, counts)], dtype=torch.int32)
+        if poison:                                       # NaN codes wherever no token lies
+            used = torch.zeros(n, ps, dtype=torch.bool)
+            for b, L in enumerate(self.lens):
+                for j in range(counts[b]):
+                    used[self.indices[self.indptr[b] + j], :min(ps, L - j * ps)] = True
+            self.codes[~used] = 0x7F
+
+    @property
+    def table(self):
+        return self.indptr, self.indices, self.last
+
+    def device(self):
+        self.dc = self.codes.view(torch.float8_e4m3fn).to(DEV)
+        self.ds = self.scales.to(DEV)
+        self.dt = tuple(t.to(DEV) for t in self.table)
+        return self
+
+    def q(self, rows, H, std=1.0):
+        return (torch.randn(rows, H, 576, generator=self.g) * std).to(torch.bfloat16)
+
+
+def _indptr(counts):
+    return torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32)
+
+
+def _codes(t):
+    return t.view(torch.uint8).cpu()
+
+
+def _check(b, q, qo, o, lse, **kw):
+    ref, ref_lse, mag, size = M8.extend(q, qo, b.codes, b.scales, *b.table, **kw)
+    o, lse = o.cpu().double(), lse.cpu().double()
+    rows = ~torch.isnan(ref_lse)
+    L = max(b.lens)
+    c = 2.0 ** -16 * (1 + size) + 2.0 ** -12 + 2.0 ** -23 * L
+    bound = c[..., None] * mag + 2.0 ** -8 * ref.abs() + 1e-30
+    assert torch.isfinite(o[rows]).all()
+    d = (o - ref).abs()
+    worst = (d / bound)[rows].max().item()
+    assert worst <= 1, f"worst |d|/bound {worst:.3f}"
+    empty = torch.isneginf(ref_lse)
+    assert torch.equal(torch.isneginf(lse) & rows, empty)
+    assert (o[empty] == 0).all()
+    fin = rows & ~empty
+    dl = (lse - ref_lse).abs()[fin] - (2.0 ** -17 * (1 + size) + 2.0 ** -21 * (1 + ref_lse.abs()))[fin]
+    assert (dl <= 0).all(), f"lse over its bound by {dl.max().item():.3e}"
+
+
+def _decode(b, q, **kw):
+    o = torch.full((q.shape[0], q.shape[1], 512), math.nan, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], math.nan, dtype=torch.float32, device=DEV)
+    B.mla_decode_fp8_fwd(q.to(DEV), b.dc, b.ds, o, *b.dt, lse=lse, **kw)
+    return o, lse
+
+
+def _extend(b, q, qo, fill=math.nan, **kw):
+    o = torch.full((q.shape[0], q.shape[1], 512), fill, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], fill, dtype=torch.float32, device=DEV)
+    B.mla_extend_fp8_fwd(q.to(DEV), qo.to(DEV), b.dc, b.ds, o, *b.dt, lse=lse, **kw)
+    return o, lse
+
+
+# ---------------------------------------------------------------- append
+def _append_and_check(b, x, counts, stride=576):
+    ip = _indptr(counts)
+    want_c, want_s = M8.append(x, ip, b.codes, b.scales, *b.table)
+    wide = torch.zeros(max(x.shape[0], 1), stride, dtype=torch.bfloat16, device=DEV)
+    wide[:x.shape[0], :576] = x.to(DEV)
+    B.mla_kv_append_fp8(wide[:x.shape[0], :576], ip.to(DEV), b.dc, b.ds, *b.dt)
+    assert torch.equal(b.ds.cpu(), want_s)
+    got = _codes(b.dc)
+    nan = (want_c & 0x7F) == 0x7F                         # a NaN's sign says nothing
+    assert torch.equal((got & 0x7F) == 0x7F, nan)
+    assert torch.equal(got[~nan], want_c[~nan])
+    b.codes, b.scales = want_c, want_s
+
+
+@pytest.mark.parametrize("ps", [1, 3, 16, 64, 130])
+@pytest.mark.parametrize("stride", [576, 640])
+def test_append_matches_the_oracle_on_ragged_batches(ps, stride):
+    new = [1, 0, 5, 64, 65, 130, 17, 1]
+    old = [0, 9, 3, 0, 63, 1, 128, 200]
+    b = Batch([n + o for n, o in zip(new, old)], ps, seed=ps, poison=False).device()
+    x = (torch.randn(sum(new), 576, generator=b.g) * 2).to(torch.bfloat16)
+    _append_and_check(b, x, new, stride)
+
+
+def test_append_grows_scales_repeatedly_and_keeps_dead_rows():
+    """Four calls on one page table that grows; magnitudes rise, fall and vanish, so pages are
+    re-coded (down to subnormal codes), kept, and started afresh over old contents."""
+    ps = 8
+    full = Batch([40, 33], ps, seed=5, poison=False).device()
+    pages = [full.indices[:5].clone(), full.indices[5:10].clone()]
+    have = [0, 0]
+    for step, (n, mag) in enumerate([((3, 1), 1e-3), ((4, 2), 5.0), ((20, 17), 1e4), ((13, 13), 0.0)]):
+        have = [h + k for h, k in zip(have, n)]
+        counts = [-(-h // ps) for h in have]
+        full.indptr = _indptr(counts)
+        full.indices = torch.cat([pages[0][:counts[0]], pages[1][:counts[1]]])
+        full.last = torch.tensor([h - (c - 1) * ps for h, c in zip(have, counts)], dtype=torch.int32)
+        full.dt = tuple(t.to(DEV) for t in full.table)
+        x = (torch.randn(sum(n), 576, generator=full.g) * mag).to(torch.bfloat16)
+        _append_and_check(full, x, n)
+
+
+def test_append_infinities_nan_zeros_and_tiny_rows():
+    b = Batch([6, 2, 3], 4, seed=9, poison=False).device()
+    x = torch.randn(11, 576, generator=b.g)
+    x[0, 5], x[1, 7], x[2, 9] = math.inf, -math.inf, math.nan
+    x[6:8] = 0.0                                          # a page of zeros: scale 0
+    x[8] = 1e-38                                          # below the smallest scale's codes
+    x[9], x[10, 0] = 0.0, 3e38
+    _append_and_check(b, x.to(torch.bfloat16), [6, 2, 3])
+    b2 = Batch([2], 4, seed=10, poison=False).device()    # nothing finite and non-zero
+    y = torch.zeros(2, 576)
+    y[0, 0], y[1, 1] = math.inf, math.nan
+    _append_and_check(b2, y.to(torch.bfloat16), [2])
+
+
+def test_append_large_page_and_many_sequences():
+    b = Batch([700], 512, seed=3, poison=False).device()  # more rows than a CTA holds in registers
+    _append_and_check(b, torch.randn(650, 576, generator=b.g).to(torch.bfloat16), [650])
+    b = Batch([1 + i % 3 for i in range(1500)], 2, seed=4, poison=False).device()
+    counts = [i % 2 for i in range(1500)]
+    _append_and_check(b, torch.randn(sum(counts), 576, generator=b.g).to(torch.bfloat16), counts)
+
+
+def test_append_and_gather_of_nothing():
+    b = Batch([3, 0], 4).device()
+    before = _codes(b.dc)
+    B.mla_kv_append_fp8(torch.empty(0, 576, dtype=torch.bfloat16, device=DEV), _indptr([0, 0]).to(DEV), b.dc, b.ds, *b.dt)
+    assert torch.equal(_codes(b.dc), before)
+    out = torch.empty(0, 576, dtype=torch.bfloat16, device=DEV)
+    assert B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, _indptr([0, 0]).to(DEV), out) is out
+
+
+# ---------------------------------------------------------------- gather
+@pytest.mark.parametrize("ps", [1, 7, 64])
+def test_gather_matches_the_oracle_and_leaves_other_rows(ps):
+    lens, take = [5, 0, 70, 33, 64, 1], [5, 0, 41, 33, 0, 1]
+    b = Batch(lens, ps, seed=ps, scale_exp=(-8, 3)).device()
+    ip = _indptr(take) + 3                                # three rows before the first sequence, some behind the last
+    out = torch.full((sum(take) + 9, 640), 5.0, dtype=torch.bfloat16)
+    dev = out.to(DEV)
+    B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, ip.to(DEV), dev[:, :576])
+    want = M8.gather(b.codes, b.scales, b.indptr, b.indices, ip, out[:, :576])
+    assert torch.equal(dev[:, :576].cpu(), want) and (dev[:, 576:] == 5).all()
+
+
+# ---------------------------------------------------------------- decode
+@pytest.mark.parametrize("ps", [1, 7, 64, 200])
+@pytest.mark.parametrize("H", [1, 8, 16, 24, 128])
+def test_decode_ragged_lengths_heads_and_pages(ps, H):
+    b = Batch([0, 1, 127, 128, 129, 2, 300, 64], ps, seed=H + ps).device()
+    q = b.q(8, H)
+    o, lse = _decode(b, q)
+    _check(b, q, torch.arange(9), o, lse)
+
+
+def test_decode_long_and_many():
+    b = Batch([3000, 5, 1711], 64, seed=1).device()
+    q = b.q(3, 16)
+    o, lse = _decode(b, q)
+    _check(b, q, torch.arange(4), o, lse)
+    b = Batch([1 + (i * 7) % 5 for i in range(700)], 2, seed=2).device()
+    q = b.q(700, 2)
+    o, lse = _decode(b, q)
+    _check(b, q, torch.arange(701), o, lse)
+
+
+def test_decode_sharp_scores_explicit_scale_and_soft_cap():
+    b = Batch([40, 300, 77, 1], 16, seed=5).device()
+    q = b.q(4, 16, std=6.0)
+    for kw in (dict(sm_scale=0.11), dict(sm_scale=0.11, logit_cap=2.0), dict(sm_scale=0.02, logit_cap=30.0)):
+        o, lse = _decode(b, q, **kw)
+        _check(b, q, torch.arange(5), o, lse, **kw)
+
+
+def test_decode_rising_scores_renormalise_every_tile():
+    """Keys whose scores rise steadily over the sequence, and the same falling: the running
+    maximum moves in every tile, or never after the first."""
+    def codes(n, ps, g):
+        c = torch.randn(n, ps, 1, 576, generator=g) * 40
+        c[:, :, 0, 0] = 400.0
+        return e4m3_encode(c)
+    for sign in (1, -1):
+        b = Batch([1000], 1, seed=6, codes=codes)
+        at = torch.arange(1000)
+        b.codes[b.indices[at].long(), 0, 0, 0] = e4m3_encode(sign * (at - 500).float() * 0.8)
+        b.device()
+        q = b.q(1, 16)
+        q[:, :, 0] = 60.0
+        o, lse = _decode(b, q)
+        _check(b, q, torch.arange(2), o, lse)
+
+
+def test_decode_one_dominant_token_over_a_long_faint_rest():
+    """A sink: one token whose score stands about 11.5 nats above 4000 others of one size."""
+    b = Batch([4001], 32, seed=7, scale_exp=(-6, -6))
+    lat = b.codes.view(torch.float8_e4m3fn)
+    b.codes[:, :, 0, 575] = e4m3_encode(torch.zeros(1))
+    first = int(b.indices[0])
+    b.codes[first, 0, 0, 575] = e4m3_encode(torch.full((1,), 256.0))
+    b.device()
+    q = torch.zeros(1, 16, 576)
+    q[:, :, 575] = 11.5 * 24 / (256 * 2.0 ** -6)
+    q[:, :, :8] = torch.randn(1, 16, 8, generator=b.g) * 0.5
+    q = q.to(torch.bfloat16)
+    o, lse = _decode(b, q)
+    _check(b, q, torch.arange(2), o, lse)
+
+
+def test_decode_pages_of_very_different_scales_and_a_zero_page():
+    b = Batch([200, 512, 40], 8, seed=8, scale_exp=(-14, 2))
+    b.scales[b.indices[3].long()] = 0.0                    # a page of zeros inside the first sequence
+    b.scales[b.indices[b.indptr[2]:].long()] = 0.0         # a sequence of nothing else
+    b.device()
+    q = b.q(3, 16, std=0.05)
+    o, lse = _decode(b, q)
+    _check(b, q, torch.arange(4), o, lse)
+
+
+def test_decode_zero_query_and_queries_of_any_size():
+    b = Batch([150, 150, 150], 16, seed=11).device()
+    q = b.q(3, 16).float()
+    q[0] = 0.0
+    q[1] *= 2.0 ** -100
+    q[2] *= 2.0 ** 40
+    q = q.to(torch.bfloat16)
+    o, lse = _decode(b, q, sm_scale=0.05 * 2.0 ** -40)
+    _check(b, q, torch.arange(4), o, lse, sm_scale=0.05 * 2.0 ** -40)
+
+
+def test_decode_nan_stays_with_its_sequence_and_head():
+    b = Batch([130, 200, 50], 16, seed=12)
+    bad = int(b.indices[b.indptr[1] + 3])
+    b.codes[bad, 2, 0, 100] = 0x7F                         # a token of the second sequence
+    b.device()
+    q = b.q(3, 16)
+    q[0, 5, 17] = math.nan
+    q[2, 7, 3] = math.inf
+    o, lse = _decode(b, q)
+    nan = torch.isnan(lse.cpu())
+    want = torch.zeros(3, 16, dtype=torch.bool)
+    want[0, 5] = want[2, 7] = True
+    want[1] = True
+    assert torch.equal(nan, want)
+    assert torch.equal(torch.isnan(o.cpu()).all(2), want) and torch.equal(torch.isnan(o.cpu()).any(2), want)
+    ref, ref_lse, mag, size = M8.decode(torch.nan_to_num(q, posinf=0.0), b.codes, b.scales, *b.table)
+    fine = ~want
+    bound = (2.0 ** -16 * (1 + size) + 2.0 ** -12 + 2.0 ** -23 * 200)[..., None] * mag + 2.0 ** -8 * ref.abs() + 1e-30
+    assert ((o.cpu().double() - ref).abs()[fine] <= bound[fine]).all()
+
+
+# ---------------------------------------------------------------- extend
+@pytest.mark.parametrize("H", [3, 16, 40, 128])
+@pytest.mark.parametrize("ps", [1, 48])
+def test_extend_ragged(ps, H):
+    lens, new = [5, 0, 140, 260, 33, 128, 9], [5, 0, 2, 37, 0, 128, 1]
+    if H == 128:
+        new = [5, 0, 2, 7, 0, 20, 1]
+    b = Batch(lens, ps, seed=ps + H).device()
+    qo = _indptr(new)
+    q = b.q(sum(new) + 3, H)                               # three rows behind the last sequence
+    o, lse = _extend(b, q, qo, fill=3.0)
+    assert (o[sum(new):] == 3).all() and (lse[sum(new):] == 3).all()
+    _check(b, q, qo, o, lse)
+
+
+def test_extend_with_more_queries_than_tokens_leaves_the_first_ones_empty():
+    b = Batch([3, 0, 130], 4, seed=2).device()
+    qo = _indptr([7, 4, 135])
+    q = b.q(146, 2)
+    o, lse = _extend(b, q, qo)
+    assert torch.isneginf(lse.cpu()[:4]).all() and torch.isneginf(lse.cpu()[7:11]).all()
+    _check(b, q, qo, o, lse)
+
+
+def test_extend_of_one_token_each_is_a_decode():
+    b = Batch([77, 300, 5], 16, seed=3).device()
+    q = b.q(3, 32)
+    o1, l1 = _decode(b, q, logit_cap=20.0)
+    o2, l2 = _extend(b, q, torch.arange(4, dtype=torch.int32), logit_cap=20.0)
+    _check(b, q, torch.arange(4), o1, l1, logit_cap=20.0)
+    _check(b, q, torch.arange(4), o2, l2, logit_cap=20.0)
+
+
+def test_extend_a_nan_token_stays_hidden_from_earlier_queries():
+    """NaN in a later token's row must not reach the queries that do not see it, though they
+    share its tile."""
+    b = Batch([140, 20], 16, seed=4)
+    page = int(b.indices[b.indptr[0] + 135 // 16])
+    b.codes[page, 135 % 16, 0, 300] = 0x7F                 # token 135 of 140
+    b.device()
+    qo = _indptr([12, 3])
+    q = b.q(15, 16)
+    o, lse = _extend(b, q, qo)
+    sees = torch.arange(12) + 129                          # token 135 is seen from 136 on
+    nan = torch.isnan(lse.cpu()).any(1)
+    assert torch.equal(nan[:12], sees >= 136) and not nan[12:].any()
+    assert torch.isnan(o.cpu()[:12][sees >= 136]).all()
+    clean = Batch([140, 20], 16, seed=4)
+    clean.codes = b.codes.clone()
+    clean.codes[page, 135 % 16, 0, 300] = 0x20
+    ref, ref_lse, mag, size = M8.extend(q, qo, clean.codes, clean.scales, *clean.table)
+    fine = ~nan
+    bound = (2.0 ** -16 * (1 + size) + 2.0 ** -12 + 2.0 ** -23 * 140)[..., None] * mag + 2.0 ** -8 * ref.abs() + 1e-30
+    assert ((o.cpu().double() - ref).abs()[fine] <= bound[fine]).all()
+
+
+# ---------------------------------------------------------------- as a user runs them
+def test_a_prompt_then_steps_then_a_prefix_read_back():
+    """Append a prompt, attend over it, append and decode token by token, read the prefix back:
+    every stage against the oracle's own cache."""
+    ps, H = 16, 16
+    b = Batch([64, 64], ps, seed=21, poison=False)
+    final = [37 + 4, 20 + 4]
+    pages = [b.indices[:4].clone(), b.indices[4:8].clone()]
+    b.device()
+
+    def grow(have):
+        counts = [-(-h // ps) for h in have]
+        b.lens = list(have)
+        b.indptr, b.indices = _indptr(counts), torch.cat([p[:c] for p, c in zip(pages, counts)])
+        b.last = torch.tensor([h - (c - 1) * ps for h, c in zip(have, counts)], dtype=torch.int32)
+        b.dt = tuple(t.to(DEV) for t in b.table)
+
+    have = [37, 20]
+    grow(have)
+    _append_and_check(b, torch.randn(57, 576, generator=b.g).to(torch.bfloat16), have)
+    q = b.q(57, H)
+    qo = _indptr(have)
+    o, lse = _extend(b, q, qo)
+    _check(b, q, qo, o, lse)
+    for step in range(4):
+        have = [h + 1 for h in have]
+        grow(have)
+        _append_and_check(b, (torch.randn(2, 576, generator=b.g) * (1 + 3 * step)).to(torch.bfloat16), [1, 1])
+        q = b.q(2, H)
+        o, lse = _decode(b, q)
+        _check(b, q, torch.arange(3), o, lse)
+    assert have == final
+    ip = _indptr([30, 24])
+    out = torch.zeros(54, 576, dtype=torch.bfloat16)
+    got = B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, ip.to(DEV), out.to(DEV))
+    assert torch.equal(got.cpu(), M8.gather(b.codes, b.scales, b.indptr, b.indices, ip, out))
+
+
+def test_same_bits_again_with_a_dirty_workspace_and_without_lse():
+    b = Batch([700, 33, 1200, 5], 16, seed=30).device()
+    q = b.q(4, 64)
+    o1, l1 = _decode(b, q)
+    need = B.mla_fp8_workspace_bytes(64, 4)
+    ws = torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    o2, l2 = _decode(b, q, workspace=ws)
+    ws.fill_(0x7F)
+    o3 = torch.empty_like(o1)
+    B.mla_decode_fp8_fwd(q.to(DEV), b.dc, b.ds, o3, *b.dt, workspace=ws)
+    assert torch.equal(o1, o2) and torch.equal(l1, l2) and torch.equal(o1, o3)
+
+
+def test_captured_step_replays_on_new_contents():
+    """An append and the attention over it, captured once and replayed with other rows, queries
+    and a page table that has grown within its buffers."""
+    ps, H = 8, 16
+    b = Batch([60, 60], ps, seed=40, poison=False).device()
+    pages = [b.indices[:8].clone(), b.indices[8:16].clone()]
+    x = torch.zeros(2, 576, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(2, H, 576, dtype=torch.bfloat16, device=DEV)
+    o = torch.zeros(2, H, 512, dtype=torch.bfloat16, device=DEV)
+    lse = torch.zeros(2, H, device=DEV)
+    ip = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    indptr = torch.zeros(3, dtype=torch.int32, device=DEV)
+    indices = torch.zeros(16, dtype=torch.int32, device=DEV)
+    last = torch.ones(2, dtype=torch.int32, device=DEV)
+
+    def step():
+        B.mla_kv_append_fp8(x, ip, b.dc, b.ds, indptr, indices, last)
+        B.mla_decode_fp8_fwd(q, b.dc, b.ds, o, indptr, indices, last, lse=lse)
+
+    def table(have):
+        counts = [-(-h // ps) for h in have]
+        b.lens, b.indptr = list(have), _indptr(counts)
+        b.indices = torch.cat([pages[0][:counts[0]], pages[1][:counts[1]]])
+        b.last = torch.tensor([h - (c - 1) * ps for h, c in zip(have, counts)], dtype=torch.int32)
+        indptr.copy_(b.indptr)
+        indices[:b.indices.numel()].copy_(b.indices)
+        last.copy_(b.last)
+
+    have = [59, 30]
+    table(have)
+    step()                                                 # warm-up outside the capture
+    torch.cuda.synchronize()
+    b.codes, b.scales = _codes(b.dc), b.ds.cpu()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for k in range(3):
+        have = [h + 1 for h in have] if k else have
+        have = [min(have[0], 60), have[1]]
+        table(have)
+        rows = (torch.randn(2, 576, generator=b.g) * (k + 1)).to(torch.bfloat16)
+        qs = b.q(2, H)
+        x.copy_(rows)
+        q.copy_(qs)
+        graph.replay()
+        torch.cuda.synchronize()
+        b.codes, b.scales = M8.append(rows, [0, 1, 2], b.codes, b.scales, *b.table)
+        assert torch.equal(_codes(b.dc), b.codes) and torch.equal(b.ds.cpu(), b.scales)
+        _check(b, qs, torch.arange(3), o, lse)
+
+
+def test_two_streams_with_a_workspace_each():
+    b = Batch([900, 411, 1300], 16, seed=50).device()
+    q = b.q(3, 32)
+    want, want_l = _decode(b, q)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(_decode(b, q))
+    torch.cuda.synchronize()
+    for o, lse in outs:
+        assert torch.equal(o, want) and torch.equal(lse, want_l)
+
+
+def test_cache_beyond_four_gigabytes():
+    """Pages whose byte offsets pass 2^32."""
+    ps = 64
+    n = (1 << 32) // (ps * 576) + 40
+    cache = torch.empty(n, ps, 1, 576, dtype=torch.float8_e4m3fn, device=DEV)
+    scale = torch.full((n, 1), 2.0 ** -6, device=DEV)
+    b = Batch([100, 200], ps, seed=60, scale_exp=(-6, -6))
+    at = torch.tensor([n - 1 - i for i in range(b.indices.numel())], dtype=torch.int32)
+    cache.view(torch.uint8)[at.long().to(DEV)] = b.codes[b.indices.long()].to(DEV)
+    table = (b.dt if hasattr(b, "dt") else tuple(t.to(DEV) for t in b.table))
+    table = (table[0], at.to(DEV), table[2])
+    q = b.q(2, 16)
+    o = torch.empty(2, 16, 512, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(2, 16, device=DEV)
+    B.mla_decode_fp8_fwd(q.to(DEV), cache, scale, o, *table, lse=lse)
+    _check(b, q, torch.arange(3), o, lse)
+    out = torch.zeros(300, 576, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_gather_fp8(cache, scale, *table, _indptr([100, 200]).to(DEV), out)
+    assert torch.equal(out.cpu(), M8.gather(b.codes, b.scales, b.indptr, b.indices, _indptr([100, 200]),
+                                            torch.zeros(300, 576, dtype=torch.bfloat16)))
+    x = torch.ones(1, 576, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_append_fp8(x, _indptr([0, 1]).to(DEV), cache, scale, *table)
+    row = cache[int(at[int(b.indptr[2]) - 1]), int(b.last[1]) - 1, 0]
+    assert (row.float() * 2.0 ** -6 == 1).all()
+
+
+# ---------------------------------------------------------------- refusals
+def test_table_entries_out_of_range_are_flagged_not_followed():
+    b = Batch([20, 30], 8, seed=70, poison=False).device()
+    q = b.q(2, 16).to(DEV)
+    o = torch.empty(2, 16, 512, dtype=torch.bfloat16, device=DEV)
+    before = _codes(b.dc)
+    x = torch.ones(2, 576, dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros(50, 576, dtype=torch.bfloat16, device=DEV)
+    ip, full = _indptr([1, 1]).to(DEV), _indptr([20, 30]).to(DEV)
+
+    def everything(table, append=ip, take=full):
+        B.mla_decode_fp8_fwd(q, b.dc, b.ds, o, *table)
+        assert B.device_status() == 32
+        B.mla_extend_fp8_fwd(q, ip, b.dc, b.ds, o, *table)
+        assert B.device_status() == 32
+        B.mla_kv_gather_fp8(b.dc, b.ds, *table, take, out)
+        assert B.device_status() == 32
+        B.mla_kv_append_fp8(x, append, b.dc, b.ds, *table)
+        assert B.device_status() == 32
+
+    for entry in (-1, b.codes.shape[0], 2 ** 31 - 1):
+        bad = b.dt[1].clone()
+        bad[2] = entry                                     # the first sequence's last page
+        everything((b.dt[0], bad, b.dt[2]))
+    assert torch.equal(_codes(b.dc)[b.indices[:2].long()], before[b.indices[:2].long()])
+    for indptr in ([0, 3, 9], [0, -1, 7], [0, 8, 7]):
+        everything((torch.tensor(indptr, dtype=torch.int32, device=DEV), b.dt[1], b.dt[2]))
+    for last in ([0, 6], [9, 6]):
+        everything((b.dt[0], b.dt[1], torch.tensor(last, dtype=torch.int32, device=DEV)))
+
+
+def test_ranges_out_of_bounds_are_flagged_not_followed():
+    b = Batch([20, 30], 8, seed=71, poison=False).device()
+    before = _codes(b.dc)
+    x = torch.ones(2, 576, dtype=torch.bfloat16, device=DEV)
+    q = b.q(2, 16).to(DEV)
+    o = torch.full((2, 16, 512), 4.0, dtype=torch.bfloat16, device=DEV)
+    out = torch.full((4, 576), 4.0, dtype=torch.bfloat16, device=DEV)
+    for bad in ([0, 1, 3], [0, -5, 2], [-2, 1, 2]):
+        ip = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        B.mla_kv_append_fp8(x, ip, b.dc, b.ds, *b.dt)
+        B.mla_extend_fp8_fwd(q, ip, b.dc, b.ds, o, *b.dt)
+        assert B.device_status() == 32
+    ip = torch.tensor([0, 21, 22], dtype=torch.int32, device=DEV)   # 21 of 20 tokens
+    big = torch.ones(22, 576, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_append_fp8(big, ip, b.dc, b.ds, *b.dt)
+    assert B.device_status() == 32
+    rows = torch.zeros(22, 576, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, ip, rows)
+    assert B.device_status() == 32 and (rows[20] == 0).all()
