@@ -114,6 +114,10 @@ int device_setup(int* sm_count) {
     if (r == cudaSuccess)
       r = cudaFuncSetAttribute(mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMlaSmemBytes);
     if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(mla_fp8_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<16>::kBytes);
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(mla_fp8_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<32>::kBytes);
+    if (r == cudaSuccess)
       r = cudaFuncSetAttribute(sort_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(sort_scatter_smem(kSortMaxExperts)));
     if (r == cudaSuccess)
@@ -1216,11 +1220,32 @@ int mla_kv_gather_fp8(const uint8_t* kv_cache, const float* kv_scale, const int3
   return check_launch(name);
 }
 
+// Workspace of the attention calls: the joining kernel's jobs, then the parts' references and
+// sums, then their accumulators, for two parts per CTA.
+static size_t lat_parts_offset() { return round_up(kLatMaxCtas * sizeof(int4), 256); }
+static size_t lat_acc_offset(int hg) { return lat_parts_offset() + round_up(2ull * kLatMaxCtas * hg * sizeof(float2), 256); }
+
 size_t mla_fp8_workspace(int num_heads, int num_q) {
-  (void)num_heads;
-  (void)num_q;
-  return 0;
+  if (num_heads < 1 || num_q < 1) return 0;
+  return lat_acc_offset(32) + 2ull * kLatMaxCtas * 32 * kLatDv * sizeof(float);
 }
+
+}  // extern "C"
+
+template <int HG>
+static int lat_launch(const char* name, LatAttnArgs a, const CUtensorMap& lat, const CUtensorMap& rot, int ctas,
+                      void* workspace, cudaStream_t st) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.merge = reinterpret_cast<int4*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + lat_parts_offset());
+  a.part_o = reinterpret_cast<float*>(ws + lat_acc_offset(HG));
+  mla_fp8_kernel<HG><<<ctas, LatSmem<HG>::kThreads, LatSmem<HG>::kBytes, st>>>(lat, rot, a);
+  if (int rc = check_launch(name)) return rc;
+  mla_fp8_join_kernel<HG><<<dim3(ctas, HG), 128, 0, st>>>(a);
+  return check_launch(name);
+}
+
+extern "C" {
 
 static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t* qo_indptr, const uint8_t* kv_cache,
                              const float* kv_scale, uint16_t* o, const int32_t* kv_indptr, const int32_t* kv_indices,
@@ -1248,7 +1273,6 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
   if (int rc = device_setup(&sms)) return rc;
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.qo_indptr = qo_indptr;
-  a.cache = kv_cache;
   a.scale = kv_scale;
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.lse = lse;
@@ -1256,8 +1280,29 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
   a.Hq = num_heads;
   a.sm_scale = sm_scale;
   a.logit_cap = logit_cap;
-  mla_fp8_simple_kernel<<<dim3(num_q, (num_heads + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return check_launch(name);
+  // rows that a page holds together come by one TMA box: the largest power of two in page_size
+  a.run = page_size % 8 ? 0 : std::min(kLatTile, page_size & -page_size);
+  CUtensorMap lat, rot;
+  std::memset(&lat, 0, sizeof(lat));
+  std::memset(&rot, 0, sizeof(rot));
+  if (num_indices > 0) {
+    const uint64_t rows = static_cast<uint64_t>(num_pages) * page_size;
+    const uint32_t box = a.run ? a.run : 1;
+    if (int rc = make_map_2d(&lat, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kv_cache, rows, kLatDk, kLatDk, 128, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B))
+      return rc;
+    if (int rc = make_map_2d(&rot, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kv_cache, rows, kLatDk, kLatDk, 64, box,
+                             CU_TENSOR_MAP_SWIZZLE_64B))
+      return rc;
+  }
+  // 16 columns per CTA where a sequence has no more, else 32; a gang of CTAs for its column groups
+  const long long cols = (static_cast<long long>(num_q) * num_heads + batch - 1) / batch;
+  const int hg = cols <= 16 ? 16 : 32;
+  a.gang = cols > 3 * hg ? 4 : cols > hg ? 2 : 1;
+  const int ctas = std::max(a.gang, std::min(sms, kLatMaxCtas) / a.gang * a.gang);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return hg == 16 ? lat_launch<16>(name, a, lat, rot, ctas, workspace, st)
+                  : lat_launch<32>(name, a, lat, rot, ctas, workspace, st);
 }
 
 int mla_decode_fp8_fwd(const uint16_t* q, const uint8_t* kv_cache, const float* kv_scale, uint16_t* o,
