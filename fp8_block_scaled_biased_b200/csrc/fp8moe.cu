@@ -1241,7 +1241,21 @@ static int lat_launch(const char* name, LatAttnArgs a, const CUtensorMap& lat, c
   a.part_o = reinterpret_cast<float*>(ws + lat_acc_offset(HG));
   mla_fp8_kernel<HG><<<ctas, LatSmem<HG>::kThreads, LatSmem<HG>::kBytes, st>>>(lat, rot, a);
   if (int rc = check_launch(name)) return rc;
-  mla_fp8_join_kernel<HG><<<dim3(ctas, HG), 128, 0, st>>>(a);
+  // launched while the attention kernel runs (programmatic dependence): it waits for its end itself
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, HG / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_fp8_join_kernel<HG>, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(FP8MOE_ECUDA, "%s: launch failed: %s", name, cudaGetErrorString(e));
+  }
   return check_launch(name);
 }
 
@@ -1298,8 +1312,8 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
   // 16 columns per CTA where a sequence has no more, else 32; a gang of CTAs for its column groups
   const long long cols = (static_cast<long long>(num_q) * num_heads + batch - 1) / batch;
   const int hg = cols <= 16 ? 16 : 32;
-  a.gang = cols > 3 * hg ? 4 : cols > hg ? 2 : 1;
-  const int ctas = std::max(a.gang, std::min(sms, kLatMaxCtas) / a.gang * a.gang);
+  a.gang_log = cols > 3 * hg ? 2 : cols > hg ? 1 : 0;
+  const int ctas = std::max(1, std::min(sms, kLatMaxCtas) >> a.gang_log) << a.gang_log;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return hg == 16 ? lat_launch<16>(name, a, lat, rot, ctas, workspace, st)
                   : lat_launch<32>(name, a, lat, rot, ctas, workspace, st);

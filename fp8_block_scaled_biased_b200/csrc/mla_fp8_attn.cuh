@@ -19,12 +19,13 @@
 // i.e. per TMEM lane) multiply the scores, and the weights before they are split.
 //
 // A CTA holds `HG` columns and walks 128-token tiles through two shared-memory stages:
-//   warp 0      page table -> TMA (boxes of 8 to 128 rows that a page holds together; gather4
-//               for other page sizes), and the tokens' scales
+//   warp 3      page table: the tiles' rows and scales, some tiles ahead
+//   warp 0      TMA: boxes of 8 to 128 rows that a page holds together; gather4 for other page
+//               sizes. A stage is loaded and freed in two halves
 //   warp 1      the MMAs: scores of the next tile are issued ahead of this tile's P V if its
 //               rows have landed, else after
-//   warp 2      the work list (below)
-//   warps 4..   one warpgroup per 16 columns, a token per thread: online softmax. The running
+//   warp 2      the work list (below), TMEM
+//   warps 4..   one warpgroup per 8 columns, a token per thread: online softmax. The running
 //               reference of a column only moves when a score passes it by more than one
 //               (base 2), and then the accumulators in TMEM are rescaled.
 //
@@ -43,11 +44,12 @@ namespace fp8moe {
 constexpr int kLatDv = 512;
 constexpr int kLatTile = 128;                              // tokens per tile
 constexpr int kLatStages = 2;
+constexpr int kLatAhead = 4;                               // tiles whose page-table entries are fetched ahead
 constexpr int kLatChunk = kLatTile * 128;                  // 128 bytes of every row of a tile
 constexpr int kLatStageBytes = kLatTile * kLatDk;          // four chunks and the 64 rotary bytes
 constexpr int kLatMaxCtas = 148;                           // one per SM
-constexpr float kLatHeadroom = 1.0f;                       // a weight may pass its reference by 2^1
-constexpr float kLatPExp = 7.0f;                           // reference weight as a code: 2^7, at most 2^8 <= 448
+constexpr float kLatHeadroom = 4.0f;                       // a weight may pass its reference by 2^4
+constexpr float kLatPExp = 4.0f;                           // reference weight as a code: 2^4, at most 2^8 <= 448
 
 struct LatAttnArgs {
   const __nv_bfloat16* q;        // [num_q, Hq, 576]
@@ -59,9 +61,14 @@ struct LatAttnArgs {
   float* part_o;                 // [2 * CTAs, HG, 512]
   float2* part_ml;               // [2 * CTAs, HG]: reference and sum
   int4* merge;                   // [CTAs]: first row, columns, parts, first part's slot (parts 0: nothing)
-  int num_q, Hq, gang;
+  int num_q, Hq, gang_log;       // CTAs of a gang: 1, 2 or 4
   int run;                       // rows per TMA box (8 .. 128), or 0: gather4
   float sm_scale, logit_cap;
+};
+
+struct LatShape {
+  int first, len, qlo, n;        // page-table entry, tokens, first query row, query tokens
+  int units, groups, tiles;      // column groups, gangs of them, tiles of each
 };
 
 // One share of one column group's tiles.
@@ -86,17 +93,24 @@ struct LatSmem {
   // TMEM columns: two score buffers, four accumulators of 128 value columns
   static constexpr int kTmemS = 0, kTmemO = 2 * kQRows;
   static constexpr int kTmemCols = (kTmemO + 4 * kPRows <= 256) ? 256 : 512;
-  static constexpr int kThreads = 128 + 128 * (HG / 16);
+  static constexpr int kGroups = HG / 8;                   // softmax warpgroups
+  static constexpr int kThreads = 128 + 128 * kGroups;
   struct Info {
     LatFragment frag[2];
-    float scale[kLatStages][kLatTile];
-    float red[HG / 16][4][16];
-    float red2[HG / 16][4][16];
-    uint64_t kv_full[kLatStages], kv_empty[kLatStages], s_full[2], s_empty[2], p_full[2], p_empty[2];
+    // per tile: first rows of the runs (or four rows per group), -1 for none; tokens' scales
+    int4 rows[kLatAhead][32];
+    float scale[kLatAhead][kLatTile];
+    int live[kLatAhead];          // rows to be loaded; -1: the end of the list
+    uint64_t tab_full[kLatAhead], tab_empty[kLatAhead];
+    float red[kGroups][4][8], inv[kGroups][8];
+    uint64_t kv_full[kLatStages][2], kv_empty[kLatStages][2];   // per half of a stage
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t frag_full[2], frag_empty[2], q_full;
+    int flag[kGroups][3];         // a score passed its reference's bound (1), a wait failed (2); tiles take turns
     long long scan[kThreads / 32];
-    long long start_off;          // position of the first sequence of this CTA's share
-    int start_b;
+    long long start_off;          // position of the first sequence of this CTA's share,
+    int start_b;                  // the sequence, and its shape
+    LatShape start;
     uint32_t tmem;
     int abort;
   };
@@ -112,28 +126,35 @@ __device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* m
       "r"(rows.w)
       : "memory");
 }
-// 32 lanes x N consecutive fp32 columns, waited for.
-__device__ __forceinline__ void tmem_load_32(uint32_t taddr, float (&v)[32]) {
-  tmem_ld_32x32b_x32(taddr, v);
-  tmem_wait_ld();
-  reg_fence_32(v);
-}
-__device__ __forceinline__ void tmem_load_16(uint32_t taddr, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+// 32 lanes x 16 consecutive fp32 columns, waited for.
+__device__ __forceinline__ void tmem_load_16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_store_16(uint32_t taddr, const float* v) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+// 16 columns and 8 more elsewhere, waited for once.
+__device__ __forceinline__ void tmem_load_16_8(uint32_t at16, uint32_t at8, float (&v)[24]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%25];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23])
+      : "r"(at16), "r"(at8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_16_8(uint32_t at16, uint32_t at8, const float (&v)[24]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%24], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n\t"
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%25], {%16,%17,%18,%19,%20,%21,%22,%23};" ::"f"(v[0]),
+      "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+      "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]),
+      "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "r"(at16), "r"(at8)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -144,7 +165,8 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint3
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1u) << 46) |
          (static_cast<uint64_t>(layout) << 61);
 }
-// Barrier of one warpgroup (named barrier `id`) that ors a predicate.
+// Barriers of one warpgroup (named barrier `id`); the second ors a predicate.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool group_any(int id, bool p) {
   uint32_t r;
   asm volatile(
@@ -153,6 +175,19 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
       : "=r"(r)
       : "r"(static_cast<uint32_t>(p)), "r"(id)
       : "memory");
+  return r != 0;
+}
+// mbar_wait, with all but the first question out of line: the roles wait in some twenty places, and
+// the kernel's code should stay small beside the instruction cache.
+__device__ __noinline__ bool lat_wait_more(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ bool lat_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try_wait(bar, parity) || lat_wait_more(bar, parity, abort);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
 // Whether a phase has completed, without waiting for it (try_wait may suspend the thread).
@@ -185,44 +220,42 @@ __device__ __forceinline__ __half2 e4m3x2_to_half2(uint16_t v) {
 }
 
 // ---------------------------------------------------------------- work list
-struct LatShape {
-  int first, len, qlo, n;        // page-table entry, tokens, first query row, query tokens
-  int units, groups, tiles;      // column groups, gangs of them, tiles of each
-};
-
 // A sequence's share of the work list; one with no query or a bad table has none.
-__device__ __forceinline__ LatShape lat_shape(const LatAttnArgs& a, int b, int HG) {
+__device__ __noinline__ LatShape lat_shape(const LatAttnArgs& a, int b, int HG) {
   LatShape s{};
-  s.qlo = b;
-  s.n = 1;
+  int qlo = b, qhi = b + 1;
   if (a.qo_indptr) {
-    const int lo = __ldg(a.qo_indptr + b), hi = __ldg(a.qo_indptr + b + 1);
-    if (lo < 0 || hi < lo || hi > a.num_q) {
-      raise_device_error(FP8MOE_DEVERR_PAGE);
-      s.n = 0;
-      return s;
-    }
-    s.qlo = lo;
-    s.n = hi - lo;
+    qlo = __ldg(a.qo_indptr + b);
+    qhi = __ldg(a.qo_indptr + b + 1);
   }
-  if (!sequence_extent(a.table, b, s.first, s.len)) s.n = 0;
-  if (s.n == 0) return s;
-  const long long cols = static_cast<long long>(s.n) * a.Hq;
-  s.units = static_cast<int>((cols + HG - 1) / HG);
-  s.groups = (s.units + a.gang - 1) / a.gang;
+  const bool table = sequence_extent(a.table, b, s.first, s.len);
+  if (qlo < 0 || qhi < qlo || qhi > a.num_q) {
+    raise_device_error(FP8MOE_DEVERR_PAGE);
+    return s;
+  }
+  if (!table || qhi == qlo) return s;
+  s.qlo = qlo;
+  s.n = qhi - qlo;
+  // at most 2^22 queries of 128 heads: fits 32 bits
+  s.units = (s.n * a.Hq + HG - 1) / HG;
+  s.groups = (s.units + (1 << a.gang_log) - 1) >> a.gang_log;
   s.tiles = max(1, (s.len + kLatTile - 1) / kLatTile);     // an empty sequence still writes its rows
   return s;
+}
+
+// Quotient of non-negative 64-bit numbers that mostly fit 32 bits.
+__device__ __noinline__ long long div_small(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
 // Warp 2, one lane: the fragments of positions [p0, p1) of the work list, through the ring.
 template <int HG>
 __device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatSmem<HG>::Info* s, long long total,
                                              int ngangs, int gang_id, int rank) {
-  const long long p0 = total * gang_id / ngangs, p1 = total * (gang_id + 1) / ngangs;
+  const long long p0 = div_small(total * gang_id, ngangs), p1 = div_small(total * (gang_id + 1), ngangs);
   int b = s->start_b;
   long long off = s->start_off;
-  LatShape sh{};
-  if (p0 < p1) sh = lat_shape(a, b, HG);
+  LatShape sh = s->start;
   int slot = 0, merge_parts = 0, merge_slot = 0, merge_row = 0, merge_cols = 0;
   uint32_t phase = 0;
   auto push = [&](const LatFragment& f) {
@@ -237,22 +270,22 @@ __device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatS
       off += static_cast<long long>(sh.groups) * sh.tiles;
       sh = lat_shape(a, ++b, HG);
     }
-    const int v = static_cast<int>((p - off) / sh.tiles);
+    const int v = static_cast<int>(div_small(p - off, sh.tiles));
     const long long base = off + static_cast<long long>(v) * sh.tiles;
     const int t0 = static_cast<int>(p - base);
     const int t1 = static_cast<int>(min(static_cast<long long>(sh.tiles), p1 - base));
     // early and late column groups in turn: what a causal mask takes from one share it takes from all
     const int g = (v & 1) ? sh.groups - 1 - v / 2 : v / 2;
-    const int u = g * a.gang + rank;
+    const int u = (g << a.gang_log) + rank;
     p = base + t1;
     if (u >= sh.units) continue;
     LatFragment f{};
     f.first = sh.first;
-    f.col0 = u * HG % a.Hq;
-    const long long c0 = static_cast<long long>(u) * HG, cols = static_cast<long long>(sh.n) * a.Hq;
-    f.cols = static_cast<int>(min(static_cast<long long>(HG), cols - c0));
-    f.row0 = static_cast<int>(static_cast<long long>(sh.qlo) * a.Hq + c0);
-    f.sees0 = sh.len - sh.n + static_cast<int>(c0 / a.Hq) + 1;
+    const int c0 = u * HG, query = c0 / a.Hq;
+    f.col0 = c0 - query * a.Hq;
+    f.cols = min(HG, sh.n * a.Hq - c0);
+    f.row0 = sh.qlo * a.Hq + c0;
+    f.sees0 = sh.len - sh.n + query + 1;
     f.len = max(0, min(sh.len, f.sees0 + (f.col0 + f.cols - 1) / a.Hq));
     const int tiles = max(1, (f.len + kLatTile - 1) / kLatTile);
     f.tile0 = t0;
@@ -264,7 +297,7 @@ __device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatS
       f.slot = 2 * blockIdx.x + (base + t0 == p0 ? 0 : 1);
       if (f.tile0 == 0) {        // the first part: this CTA's entry for the joining kernel
         const long long last = base + tiles - 1;           // the gang that holds the last tile
-        merge_parts = static_cast<int>(((last + 1) * ngangs + total - 1) / total - 1) - gang_id + 1;
+        merge_parts = static_cast<int>(div_small((last + 1) * ngangs + total - 1, total)) - gang_id;
         merge_slot = f.slot;
         merge_row = f.row0;
         merge_cols = f.cols;
@@ -277,14 +310,15 @@ __device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatS
 }
 
 // ---------------------------------------------------------------- softmax warpgroup
-// Codes of columns 2i and 2i + 1 (two bytes) of the three terms of y in [0, 2^8].
+// Codes of two columns (two bytes) of the three terms of y in [0, 2^8]: y is rounded to the 11 bits
+// of fp16, of which hi takes 4, lo 4 and lo2 the rest, exactly (down to lo2's subnormals).
 __device__ __forceinline__ void split_weights(float y0, float y1, uint16_t& hi, uint16_t& lo, uint16_t& lo2) {
-  hi = cvt_e4m3x2(y0, y1);
-  const float2 h = __half22float2(e4m3x2_to_half2(hi));
-  // the rest is within half a step of hi: exact in fp32, 11 bits of it in fp16 (times 32: at most 256)
-  const __half2 r = __floats2half2_rn((y0 - h.x) * 32.0f, (y1 - h.y) * 32.0f);
+  const __half2 k32 = __float2half2_rn(32.0f);
+  const __half2 y = __floats2half2_rn(y0, y1);
+  hi = half2_to_e4m3x2(y);
+  const __half2 r = __hmul2(__hsub2(y, e4m3x2_to_half2(hi)), k32);     // at most half a step of hi: 8 * 32
   lo = half2_to_e4m3x2(r);
-  lo2 = half2_to_e4m3x2(__hmul2(__hsub2(r, e4m3x2_to_half2(lo)), __float2half2_rn(32.0f)));
+  lo2 = half2_to_e4m3x2(__hmul2(__hsub2(r, e4m3x2_to_half2(lo)), k32));
 }
 
 __device__ __forceinline__ int float_order(float x) {      // order of floats as order of ints
@@ -293,23 +327,83 @@ __device__ __forceinline__ int float_order(float x) {      // order of floats as
 }
 __device__ __forceinline__ float order_float(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
 
+// One of a thread's columns chosen by a runtime index, without indexing registers.
+__device__ __forceinline__ float pick8(const float (&v)[8], int i) {
+  float x = v[0];
+#pragma unroll
+  for (int c = 1; c < 8; ++c) x = i == c ? v[c] : x;
+  return x;
+}
+
+// Splits this warpgroup's 8 query columns into their two terms (16 threads per column, 36 entries
+// each) and stores them as the score MMAs' B operand: core matrices of 8 rows x 16 bytes, rows
+// 16 g .. 16 g + 7 the high terms, the next 8 the low ones. Returns the scale of column tid / 16:
+// NaN for a row with an entry that is not finite, which makes all its scores NaN whatever its codes
+// are. (The second pass reads L1 again: registers cannot be indexed in a loop, and unrolled code
+// costs more in instruction fetches than it saves.)
+template <int HG>
+__device__ __forceinline__ float lat_load_queries(const LatAttnArgs& a, const LatFragment& f, uint8_t* qs, int group,
+                                                  int tid) {
+  using SM = LatSmem<HG>;
+  const int c = group * 8 + (tid >> 4), part = tid & 15;
+  const bool live = c < f.cols;
+  const uint2* src = reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(f.row0) + (live ? c : 0)) * kLatDk) + part;
+  uint32_t mx = 0;
+  {
+    uint2 x[9];
+#pragma unroll
+    for (int j = 0; j < 9; ++j) x[j] = __ldg(src + 16 * j);
+#pragma unroll
+    for (int j = 0; j < 9; ++j) mx = __vmaxu2(mx, __vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu));
+  }
+  mx = max(mx & 0xffffu, mx >> 16);
+  for (int d = 1; d < 16; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  if (!live) mx = 0;
+  const int ex = max(kScaleMinExp, static_cast<int>(mx >> 7) - 135 + ((mx & 0x7fu) > 96u ? 1 : 0));
+  const float inv = live ? __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.0f;
+  const __half2 k16 = __float2half2_rn(16.0f);
+  uint8_t* dst = qs + (part >> 2) * (SM::kQRows * 16) + (part & 3) * 4 + (group * 16 + (tid >> 4)) * 16;
+  uint2 x = __ldg(src);
+#pragma unroll 1
+  for (int j = 0; j < 9; ++j) {
+    const float2 v0 = bf16x2_to_float(x.x), v1 = bf16x2_to_float(x.y);
+    if (j < 8) x = __ldg(src + 16 * (j + 1));
+    const __half2 h0 = __floats2half2_rn(v0.x * inv, v0.y * inv), h1 = __floats2half2_rn(v1.x * inv, v1.y * inv);
+    const uint16_t hi0 = half2_to_e4m3x2(h0), hi1 = half2_to_e4m3x2(h1);           // at most 448: h exact above 2^-16
+    const uint16_t lo0 = half2_to_e4m3x2(__hmul2(__hsub2(h0, e4m3x2_to_half2(hi0)), k16));
+    const uint16_t lo1 = half2_to_e4m3x2(__hmul2(__hsub2(h1, e4m3x2_to_half2(hi1)), k16));
+    *reinterpret_cast<uint32_t*>(dst) = hi0 | (static_cast<uint32_t>(hi1) << 16);
+    *reinterpret_cast<uint32_t*>(dst + 128) = lo0 | (static_cast<uint32_t>(lo1) << 16);
+    dst += 4 * (SM::kQRows * 16);                          // 64 entries on
+  }
+  return mx >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+}
+
 template <int HG>
 __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename LatSmem<HG>::Info* s, uint8_t* smem,
                                                  uint32_t tmem) {
   using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
-  const int tid = threadIdx.x & 127, group = (threadIdx.x >> 7) - 1;   // warpgroup of 16 columns
+  const int tid = threadIdx.x & 127, group = (threadIdx.x >> 7) - 1;   // warpgroup of 8 columns
   const int warp = tid >> 5, lane = tid & 31;
   const int bar_id = 1 + group;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  // The terms of two groups' weights share 48 N columns: hi and lo of the first, both lo2, hi and lo
+  // of the second; 16 bytes of a token's weights are one block of 16 N columns.
+  const int block = 3 * (group >> 1) + 2 * (group & 1), block2 = 3 * (group >> 1) + 1, half8 = 8 * (group & 1);
+  const uint32_t acc_hi = lane_base + SM::kTmemO + 16 * block, acc_lo2 = lane_base + SM::kTmemO + 16 * block2 + half8;
   const float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   const bool capped = a.logit_cap > 0.0f;
+  // cap * tanh(t / cap) * log2(e) = cap2 - 2 cap2 / (1 + 2^(t cap_in)): off by a few 2^-24 of the cap
+  const float cap2 = a.logit_cap * kLog2e, cap_in = 2.0f * kLog2e / a.logit_cap;
+  volatile int* flag = &s->flag[group][0];
   int fslot = 0;
   uint32_t fphase = 0;
   int it = 0;                                              // tiles so far: buffers and phases follow it
+  int turn = 0;                                            // it % 3
 
   for (;;) {
-    bool ok = mbar_wait(&s->frag_full[fslot], fphase, abort_flag);
+    bool ok = lat_wait(&s->frag_full[fslot], fphase, abort_flag);
     if (group_any(bar_id, !ok)) return false;
     const LatFragment f = s->frag[fslot];
     __syncwarp();
@@ -317,172 +411,141 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
     if (!f.valid) return true;
 
-    // ---- the queries: eight threads per column, 72 entries each. The earlier fragment's score
-    // MMAs are done (its last s_full was waited for), so their operand may be overwritten.
-    float qf;                                              // of column tid / 8
-    {
-      const int c = group * 16 + (tid >> 3), part = tid & 7;
-      const bool live = c < f.cols;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(f.row0) + (live ? c : 0)) * kLatDk) + part;
-      uint4 x[9];
-#pragma unroll
-      for (int j = 0; j < 9; ++j) x[j] = live ? __ldg(src + 8 * j) : make_uint4(0, 0, 0, 0);
-      uint32_t mx = 0;
-#pragma unroll
-      for (int j = 0; j < 9; ++j)
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(finite_magnitudes(x[j].x), finite_magnitudes(x[j].y)),
-                                   __vmaxu2(finite_magnitudes(x[j].z), finite_magnitudes(x[j].w))));
-      mx = max(mx & 0xffffu, mx >> 16);
-      for (int d = 1; d < 8; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      const int ex = max(kScaleMinExp, static_cast<int>(mx >> 7) - 135 + ((mx & 0x7fu) > 96u ? 1 : 0));
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-      qf = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-      uint8_t* qs = smem + SM::kOffQ;
-      const int row_hi = group * 32 + (tid >> 3);          // the terms of 16 columns lie together
-#pragma unroll
-      for (int j = 0; j < 9; ++j) {
-        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        uint16_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2 v = bf16x2_to_float(w[i]);
-          v.x *= inv;
-          v.y *= inv;
-          if (isinf(v.x)) v.x = NAN;                       // no code is infinite
-          if (isinf(v.y)) v.y = NAN;
-          hi[i] = cvt_e4m3x2(v.x, v.y);
-          const float2 h = __half22float2(e4m3x2_to_half2(hi[i]));
-          lo[i] = cvt_e4m3x2((v.x - h.x) * 16.0f, (v.y - h.y) * 16.0f);
-        }
-        // 8-byte pieces of core matrices of 8 rows x 16 bytes
-        const int k = (j * 8 + part) * 8;
-        uint8_t* dst = qs + (k >> 4) * (SM::kQRows * 16) + (k & 8);
-        *reinterpret_cast<uint2*>(dst + row_hi * 16) =
-            make_uint2(hi[0] | (static_cast<uint32_t>(hi[1]) << 16), hi[2] | (static_cast<uint32_t>(hi[3]) << 16));
-        *reinterpret_cast<uint2*>(dst + (row_hi + 16) * 16) =
-            make_uint2(lo[0] | (static_cast<uint32_t>(lo[1]) << 16), lo[2] | (static_cast<uint32_t>(lo[3]) << 16));
-      }
-      if (part == 0) s->red[group][0][tid >> 3] = qf * (a.sm_scale * (capped ? 1.0f : kLog2e));
-      fence_proxy_async_smem();
-    }
+    // The earlier fragment's score MMAs are done (its last s_full was waited for): their operand
+    // may be overwritten.
+    const float qscale = lat_load_queries<HG>(a, f, smem + SM::kOffQ, group, tid);
+    if ((tid & 15) == 0) s->inv[group][tid >> 4] = qscale * (a.sm_scale * (capped ? 1.0f : kLog2e));
+    fence_proxy_async_smem();
     if (group_any(bar_id, false)) return false;
     if (tid == 0) mbar_arrive(&s->q_full);
-    float fac[16], ref[16], sum[16];
+    float fac[8], nref[8], sum[8];                         // nref: code exponent of the reference minus the reference
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      fac[c] = s->red[group][0][c];
-      ref[c] = -INFINITY;
+    for (int c = 0; c < 8; ++c) {
+      fac[c] = s->inv[group][c];
+      nref[c] = INFINITY;
       sum[c] = 0.0f;
     }
-    const int sees_min = f.sees0 + (f.col0 + group * 16) / a.Hq;       // of this group's first column
-    const int col = f.col0 + group * 16;
+    const int query = (f.col0 + group * 8) / a.Hq;
+    const int sees_min = f.sees0 + query;                  // of this group's first column
+    const int next_query = (query + 1) * a.Hq - (f.col0 + group * 8);  // columns until the next query
 
-    for (int tile = f.tile0; tile < f.tile1; ++tile, ++it) {
+    for (int tile = f.tile0; tile < f.tile1; ++tile, ++it, turn = turn == 2 ? 0 : turn + 1) {
       const int buf = it & 1, stage = it % kLatStages;
-      const uint32_t phase = (it >> 1) & 1, kv_phase = (it / kLatStages) & 1;
-      ok = mbar_wait(&s->s_full[buf], phase, abort_flag) && mbar_wait(&s->kv_full[stage], kv_phase, abort_flag) &&
-           mbar_wait(&s->p_empty[buf], phase ^ 1u, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      const float sc = s->scale[stage][tid];
-      tc_fence_after();
-      float v[32];
-      tmem_load_32(lane_base + SM::kTmemS + buf * SM::kQRows + group * 32, v);
-      tc_fence_before();
+      const uint32_t phase = (it >> 1) & 1;
+      const int ahead = it % kLatAhead;
+      ok = lat_wait(&s->tab_full[ahead], (it / kLatAhead) & 1, abort_flag);
+      const float sc = s->scale[ahead][tid];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s->s_empty[buf]);
-      float t[16];
-      bool bad = true;                                     // a NaN in this token's row makes every score NaN
+      if (lane == 0) mbar_arrive(&s->tab_empty[ahead]);
+      // the reference of a column bounds score + log2(page scale): the weights that meet the codes
+      const float bound = kLatPExp + kLatHeadroom - (sc > 0.0f ? __log2f(sc) : -100.0f);
+      float fs[8];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        t[c] = (v[c] + v[16 + c] * 0.0625f) * (fac[c] * sc);
-        bad = bad && isnan(t[c]);
+      for (int c = 0; c < 8; ++c) fs[c] = fac[c] * sc;
+      ok = lat_wait(&s->s_full[buf], phase, abort_flag) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      float t[8];
+      {
+        float v[16];
+        tmem_load_16(lane_base + SM::kTmemS + buf * SM::kQRows + group * 16, v);
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(&s->s_empty[buf]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) t[c] = fmaf(v[8 + c], 0.0625f, v[c]) * fs[c];
+      }
+      bool bad = false;                                    // a NaN in this token's row: every score is NaN
+      if (isnan(t[0])) {
+        bad = true;
+#pragma unroll
+        for (int c = 1; c < 8; ++c) bad = bad && isnan(t[c]);
       }
       if (capped) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) t[c] = a.logit_cap * tanhf(t[c] / a.logit_cap) * kLog2e;
+        for (int c = 0; c < 8; ++c) t[c] = cap2 - 2.0f * cap2 * __fdividef(1.0f, 1.0f + exp2_fast(t[c] * cap_in));
       }
       const int pos = tile * kLatTile + tid;
-      if ((tile + 1) * kLatTile > sees_min || (tile + 1) * kLatTile > f.len) {
-        int sees = sees_min, left = a.Hq - col % a.Hq;     // columns until the next query
+      if ((tile + 1) * kLatTile > min(sees_min, f.len)) {
+        int sees = sees_min, left = next_query;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < 8; ++c) {
           if (pos >= min(sees, f.len)) t[c] = -INFINITY;
           if (--left == 0) { left = a.Hq; ++sees; }
         }
       }
-      // the reference of a column bounds score + log2(page scale): the weights that meet the codes
-      const float lg = sc > 0.0f ? log2f(sc) : -100.0f;
-      bool over = false;
+      // the weights' exponents, and whether one passes its bound (fmaxf passes over NaN; a column that
+      // has no reference yet raises the flag with its first finite score)
+      float w[8], top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) over = over || (t[c] + lg > ref[c] + kLatHeadroom);
-      if (group_any(bar_id, over || !ok)) {
-        if (group_any(bar_id, !ok)) return false;
+      for (int c = 0; c < 8; ++c) {
+        w[c] = t[c] + nref[c];
+        top = fmaxf(top, t[c] == -INFINITY ? -INFINITY : w[c]);
+      }
+      // A raised flag is read after the barrier below; until then the weights are computed as if there
+      // were none.
+      if (!ok) flag[turn] = 2;
+      else if (top > bound) atomicOr(const_cast<int*>(&flag[turn]), 1);
+      uint32_t hi[2], lo[2], lo2[2];
+      for (bool again = false;; again = true) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = exp2_fast(t[c] == -INFINITY ? -INFINITY : w[c]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint16_t h[2], l[2], l2[2];
+          split_weights(w[4 * i] * sc, w[4 * i + 1] * sc, h[0], l[0], l2[0]);
+          split_weights(w[4 * i + 2] * sc, w[4 * i + 3] * sc, h[1], l[1], l2[1]);
+          hi[i] = h[0] | (static_cast<uint32_t>(h[1]) << 16);
+          lo[i] = l[0] | (static_cast<uint32_t>(l[1]) << 16);
+          lo2[i] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
+        }
+        if (again) break;
+        ok = lat_wait(&s->p_empty[buf], phase ^ 1u, abort_flag);       // the P V two tiles ago is done
+        if (!ok) flag[turn] = 2;
+        group_sync(bar_id);
+        const int raised = flag[turn];
+        if (raised & 2) return false;
+        if (!raised) break;
         // new references: the largest over the tile, where that is larger
+        const float lg = kLatPExp + kLatHeadroom - bound;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < 8; ++c) {
           const float x = isnan(t[c]) ? -INFINITY : t[c] + lg;
           const int m = __reduce_max_sync(0xffffffffu, float_order(x));
-          if (lane == 0) s->red2[group][warp][c] = order_float(m);
+          if (lane == 0) s->red[group][warp][c] = order_float(m);
         }
-        if (group_any(bar_id, false)) return false;
-        float alpha[16];
+        ok = tile == f.tile0 || lat_wait(&s->p_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort_flag);
+        if (group_any(bar_id, !ok)) return false;
+        float alpha[8];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float m = fmaxf(fmaxf(s->red2[group][0][c], s->red2[group][1][c]),
-                                fmaxf(s->red2[group][2][c], s->red2[group][3][c]));
-          const float next = fmaxf(ref[c], m);
-          alpha[c] = next == -INFINITY ? 1.0f : exp2_fast(ref[c] - next);
-          ref[c] = next;
+        for (int c = 0; c < 8; ++c) {
+          const float m = fmaxf(fmaxf(s->red[group][0][c], s->red[group][1][c]),
+                                fmaxf(s->red[group][2][c], s->red[group][3][c]));
+          const float next = fminf(nref[c], kLatPExp - m); // m = -inf: as it was
+          alpha[c] = next == INFINITY ? 1.0f : exp2_fast(next - nref[c]);
+          nref[c] = next;
           sum[c] *= alpha[c];
+          w[c] = t[c] + next;
         }
         if (tile > f.tile0) {                              // what has been summed, in the new references
-          ok = mbar_wait(&s->p_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort_flag);
-          if (group_any(bar_id, !ok)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
+            float x[24];
+            tmem_load_16_8(acc_hi + m * SM::kPRows, acc_lo2 + m * SM::kPRows, x);
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
-              const uint32_t at = lane_base + SM::kTmemO + m * SM::kPRows + group * 48 + term * 16;
-              float w[16];
-              tmem_load_16(at, w);
-#pragma unroll
-              for (int c = 0; c < 16; ++c) w[c] *= alpha[c];
-              tmem_store_16(at, w);
-            }
+            for (int i = 0; i < 24; ++i) x[i] *= alpha[i & 7];
+            tmem_store_16_8(acc_hi + m * SM::kPRows, acc_lo2 + m * SM::kPRows, x);
           }
           tmem_wait_st();
           tc_fence_before();
         }
-        if (group_any(bar_id, false)) return false;        // red2 may be written again
+        group_sync(bar_id);                                // red may be written again
       }
-      // weights, their sum, and their codes: 16 bytes per term and token
-      uint32_t code[3][4];
-      const float gain = sc;
-#pragma unroll
-      for (int c = 0; c < 16; c += 2) {
-        const float r0 = ref[c] == -INFINITY ? 0.0f : ref[c], r1 = ref[c + 1] == -INFINITY ? 0.0f : ref[c + 1];
-        const float p0 = exp2_fast(t[c] - r0 + kLatPExp), p1 = exp2_fast(t[c + 1] - r1 + kLatPExp);
-        sum[c] += p0;
-        sum[c + 1] += p1;
-        uint16_t hi, lo, lo2;
-        split_weights(p0 * gain, p1 * gain, hi, lo, lo2);
-        const int w = c >> 2, sh = (c & 2) * 8;
-        if (sh == 0) {
-          code[0][w] = hi;
-          code[1][w] = lo;
-          code[2][w] = lo2;
-        } else {
-          code[0][w] |= static_cast<uint32_t>(hi) << 16;
-          code[1][w] |= static_cast<uint32_t>(lo) << 16;
-          code[2][w] |= static_cast<uint32_t>(lo2) << 16;
-        }
-      }
-      uint8_t* pb = smem + SM::kOffP + buf * SM::kPBytes + group * 3 * (16 * kLatTile) + tid * 16;
-#pragma unroll
-      for (int term = 0; term < 3; ++term)
-        *reinterpret_cast<uint4*>(pb + term * (16 * kLatTile)) =
-            make_uint4(code[term][0], code[term][1], code[term][2], code[term][3]);
+      // the flag of the tile after the next: read before this barrier, raised after the next one
+      if (tid == 0) flag[turn == 0 ? 2 : turn - 1] = 0;
+      uint8_t* pb = smem + SM::kOffP + buf * SM::kPBytes + tid * 16;
+      *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(pb + block2 * (16 * kLatTile) + half8) = make_uint2(lo2[0], lo2[1]);
       if (bad) {
         // the row must not reach columns that give it no weight (0 x NaN): its values become 0, the
         // weights of the columns that do see it are NaN themselves
@@ -494,60 +557,252 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->p_full[buf]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[c] += w[c];
     }
 
     // ---- the fragment's result: the columns' sums over all threads, then the accumulators
-    const int lastbuf = (it - 1) & 1;
-    ok = mbar_wait(&s->p_empty[lastbuf], ((it - 1) >> 1) & 1, abort_flag);
+    ok = lat_wait(&s->p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag);
+    // lane bits 4 .. 2 choose a half of the columns each: four lanes end with parts of one column's sum
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float x = sum[c];
-      for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      if (lane == 0) s->red2[group][warp][c] = x;
+    for (int h = 4; h; h >>= 1) {
+      const bool upper = (lane & (4 * h)) != 0;
+#pragma unroll
+      for (int c = 0; c < h; ++c) {
+        const float keep = upper ? sum[c + h] : sum[c], give = upper ? sum[c] : sum[c + h];
+        sum[c] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * h);
+      }
     }
+    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
+    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+    if ((lane & 3) == 0) s->red[group][warp][lane >> 2] = sum[0];
     if (group_any(bar_id, !ok)) return false;
-#pragma unroll
-    for (int c = 0; c < 16; ++c)
-      sum[c] = (s->red2[group][0][c] + s->red2[group][1][c]) + (s->red2[group][2][c] + s->red2[group][3][c]);
     tc_fence_after();
-    const int live = min(16, f.cols - group * 16);
-    const size_t row0 = static_cast<size_t>(f.row0) + group * 16;
-    const size_t part0 = static_cast<size_t>(max(f.slot, 0)) * HG + group * 16;
+    const int live = min(8, f.cols - group * 8);
+    const size_t row0 = static_cast<size_t>(f.row0) + group * 8;
+    const size_t part0 = static_cast<size_t>(max(f.slot, 0)) * HG + group * 8;
+    if (tid < 8) {
+      const float l = (s->red[group][0][tid] + s->red[group][1][tid]) + (s->red[group][2][tid] + s->red[group][3][tid]);
+      const float m = pick8(nref, tid);                    // l sums 2^(score + m)
+      if (tid < live) {
+        if (f.slot >= 0) a.part_ml[part0 + tid] = make_float2(m, l);
+        else if (a.lse) a.lse[row0 + tid] = l == 0.0f ? -INFINITY : (log2f(l) - (m == INFINITY ? 0.0f : m)) * kLn2;
+      }
+      // what the accumulators are multiplied by: a part stays as it is
+      s->inv[group][tid] = f.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+    }
+    group_sync(bar_id);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sum[c] = s->inv[group][c];
 #pragma unroll 1
     for (int m = 0; m < 4; ++m) {
-      float acc[16], w[16];
-      const uint32_t at = lane_base + SM::kTmemO + m * SM::kPRows + group * 48;
-      tmem_load_16(at + 32, acc);
-      tmem_load_16(at + 16, w);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) acc[c] = w[c] + acc[c] * 0.03125f;
-      tmem_load_16(at, w);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) acc[c] = w[c] + acc[c] * 0.03125f;
+      float x[24];
+      tmem_load_16_8(acc_hi + m * SM::kPRows, acc_lo2 + m * SM::kPRows, x);
       const int d = m * 128 + tid;
-      if (f.slot < 0) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c < live)
-            a.o[(row0 + c) * kLatDv + d] = __float2bfloat16(sum[c] == 0.0f ? 0.0f : acc[c] / sum[c]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c < live) a.part_o[(part0 + c) * kLatDv + d] = acc[c];
+      for (int c = 0; c < 8; ++c) {
+        const float y = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]);
+        if (c < live) {
+          if (f.slot < 0) a.o[(row0 + c) * kLatDv + d] = __float2bfloat16(sum[c] == 0.0f ? 0.0f : y * sum[c]);
+          else a.part_o[(part0 + c) * kLatDv + d] = y;
+        }
       }
     }
     tc_fence_before();
-    if (tid < 16 && tid < live) {
-      float m = 0.0f, l = 0.0f;
+    group_sync(bar_id);                                    // red, inv and TMEM are read before what comes next
+  }
+}
+
+// ---------------------------------------------------------------- MMA warp
+// The whole warp runs the loop and one elected lane issues, so that descriptors stay in uniform
+// registers: 44 and 48 cycles per MMA (16 columns), 70 from a divergent branch. Every turn asks all
+// barriers that matter at once, a lane each: the halves of the next tile's rows, its score buffer,
+// this tile's weights.
+template <int HG>
+__device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint8_t* smem, uint32_t tmem_any) {
+  using SM = LatSmem<HG>;
+  volatile int* abort_flag = &s->abort;
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kIdescS = umma_idesc_e4m3_f32(128, SM::kQRows);
+  constexpr uint32_t kIdescO = umma_idesc_e4m3_f32(128, SM::kPRows) | (1u << 15) | (1u << 16);   // A and B M/N-major
+  const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
+  const uint64_t desc_k = umma_desc(base, 16, 1024, 2);                            // rows of 128 bytes, K-major
+  const uint64_t desc_rot = umma_desc(base + 4 * kLatChunk, 16, 512, 4);           // rows of 64 bytes
+  const uint64_t desc_q = umma_desc(base + SM::kOffQ, SM::kQRows * 16, 128, 0);
+  const uint64_t desc_v = umma_desc(base, 1024, 1024, 2);                          // the same rows, M-major
+  const uint64_t desc_p = umma_desc(base + SM::kOffP, 128, 16 * kLatTile, 0);
+  const bool leader = elect_one();
+  int it0 = 0, fslot = 0, fcount = 0;
+  uint32_t fphase = 0;
+  for (;;) {
+    if (!__all_sync(0xffffffffu, lat_wait(&s->frag_full[fslot], fphase, abort_flag))) return false;
+    const int n = __shfl_sync(0xffffffffu, s->frag[fslot].valid ? s->frag[fslot].tile1 - s->frag[fslot].tile0 : 0, 0);
+    if (leader) mbar_arrive(&s->frag_empty[fslot]);
+    if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
+    if (n == 0) return true;
+    if (!__all_sync(0xffffffffu, lat_wait(&s->q_full, fcount & 1, abort_flag))) return false;
+    ++fcount;
+    int qk = 0, pv = 0;
+    unsigned long long t0 = 0;
+    for (uint32_t spin = 0; pv < n; ++spin) {
+      const int i = it0 + qk, stage = i % kLatStages, buf = i & 1;
+      const int j = it0 + pv, pstage = j % kLatStages, pbuf = j & 1;
+      uint64_t* bar = lane < 2 ? &s->kv_full[stage][lane] : lane == 2 ? &s->s_empty[buf] : &s->p_full[pbuf];
+      const uint32_t parity = lane < 2 ? (i / kLatStages) & 1 : lane == 2 ? ((i >> 1) & 1) ^ 1u : (j >> 1) & 1;
+      const uint32_t ready = __ballot_sync(0xffffffffu, mbar_test(bar, parity));
+      const bool do_qk = qk < n && qk <= pv + 1 && (ready & 7u) == 7u;
+      const bool do_pv = pv < qk && (ready & 8u) != 0;
+      if (do_qk || do_pv) tc_fence_after();
+      if (do_pv) {
+        if (leader) {
+          const uint64_t kv = static_cast<uint64_t>(pstage * kLatStageBytes) >> 4;
+          const uint64_t p = desc_p + (pbuf * (SM::kPBytes >> 4));
+          const uint32_t more = pv > 0 ? 1u : 0u;
 #pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (c == tid) { m = ref[c]; l = sum[c]; }
-      if (f.slot >= 0) {
-        a.part_ml[part0 + tid] = make_float2(m, l);
-      } else if (a.lse) {
-        a.lse[row0 + tid] = l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kLatPExp + log2f(l)) * kLn2;
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_f8(tmem + SM::kTmemO + m * SM::kPRows, desc_v + kv + m * (kLatChunk >> 4) + k * 256, p + k * 32,
+                      kIdescO, k > 0 ? 1u : more);
+            if (m & 1) umma_commit(&s->kv_empty[pstage][m >> 1]);
+          }
+          umma_commit(&s->p_empty[pbuf]);
+        }
+        __syncwarp();
+        ++pv;
+        spin = 0;
+      }
+      if (do_qk) {
+        if (leader) {
+          const uint64_t kv = static_cast<uint64_t>(stage * kLatStageBytes) >> 4;
+          const uint32_t d = tmem + SM::kTmemS + buf * SM::kQRows;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            umma_f8(d, desc_rot + kv + k * 2, desc_q + (32 + k * 2) * SM::kQRows, kIdescS, k > 0 ? 1u : 0u);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_f8(d, desc_k + kv + c * (kLatChunk >> 4) + k * 2, desc_q + (c * 8 + k * 2) * SM::kQRows, kIdescS, 1u);
+          umma_commit(&s->s_full[buf]);
+        }
+        __syncwarp();
+        ++qk;
+        spin = 0;
+      }
+      if (spin == 64) t0 = global_timer_ns();
+      if ((spin & 1023u) == 1023u && __any_sync(0xffffffffu, *abort_flag || global_timer_ns() - t0 > kWaitLimitNs))
+        return false;
+    }
+    it0 += n;
+  }
+}
+
+// ---------------------------------------------------------------- page table and row loads
+// Warp 3: the rows and scales of the tiles, some tiles ahead of their loads. A lane looks up a run
+// of rows (or four single ones) and writes four tokens' scales.
+template <int HG>
+__device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename LatSmem<HG>::Info* s) {
+  volatile int* abort_flag = &s->abort;
+  const int lane = threadIdx.x & 31;
+  const int ps = a.table.page_size, run = a.run;
+  int slot = 0, fslot = 0;
+  uint32_t phase = 0, fphase = 0;
+  for (;;) {
+    if (!__all_sync(0xffffffffu, lat_wait(&s->frag_full[fslot], fphase, abort_flag))) return false;
+    const LatFragment f = s->frag[fslot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s->frag_empty[fslot]);
+    if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
+    const int tile1 = f.valid ? f.tile1 : f.tile0 + 1;      // the end takes an entry too
+    for (int tile = f.tile0; tile < tile1; ++tile) {
+      const int tok = tile * kLatTile;
+      int4 rows = make_int4(-1, -1, -1, -1);
+      float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (run) {
+        const int pos = tok + lane * run;
+        float one = 0.0f;
+        if (lane < kLatTile / run && pos < f.len) {
+          const int at = pos / ps, page = table_page(a.table, f.first + at);
+          if (page >= 0) {
+            rows.x = page * ps + (pos - at * ps);
+            one = __ldg(a.scale + page);
+          }
+        }
+        one = __shfl_sync(0xffffffffu, one, 4 * lane / run);
+        sc = make_float4(one, one, one, one);
+      } else {
+        const int pos = tok + 4 * lane;
+        int* r = reinterpret_cast<int*>(&rows);
+        float* c = reinterpret_cast<float*>(&sc);
+        int seen = -1;                                     // a row past the end, or of a bad page, repeats another
+        if (pos < f.len) {
+          int at = pos / ps, off = pos - at * ps;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int page = table_page(a.table, f.first + at);
+            if (page >= 0) {
+              r[i] = page * ps + off;
+              c[i] = __ldg(a.scale + page);
+              seen = r[i];
+            }
+            if (pos + i + 1 < f.len && ++off == ps) { off = 0; ++at; }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (r[i] < 0) r[i] = seen;
+        }
+      }
+      const int live = __popc(__ballot_sync(0xffffffffu, rows.x >= 0)) * (run ? run : 4);
+      if (!__all_sync(0xffffffffu, lat_wait(&s->tab_empty[slot], phase ^ 1u, abort_flag))) return false;
+      s->rows[slot][lane] = rows;
+      *reinterpret_cast<float4*>(&s->scale[slot][4 * lane]) = sc;
+      if (lane == 0) s->live[slot] = f.valid ? live : -1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s->tab_full[slot]);
+      if (++slot == kLatAhead) { slot = 0; phase ^= 1u; }
+    }
+    if (!f.valid) return true;
+  }
+}
+
+// Warp 0, one thread: the loads, a half of a stage at a time as P V frees them.
+template <int HG>
+__device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtensorMap* tm_lat, const CUtensorMap* tm_rot,
+                                              typename LatSmem<HG>::Info* s, uint8_t* smem) {
+  volatile int* abort_flag = &s->abort;
+  const int run = a.run, step = run ? run : 4, pieces = kLatTile / step;
+  for (int it = 0;; ++it) {
+    const int stage = it % kLatStages, ahead = it % kLatAhead;
+    const uint32_t free_phase = ((it / kLatStages) & 1) ^ 1u;
+    if (!lat_wait(&s->tab_full[ahead], (it / kLatAhead) & 1, abort_flag)) return false;
+    const int live = s->live[ahead];
+    if (live < 0) return true;
+    uint8_t* dst = smem + stage * kLatStageBytes;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {                 // rotary entries and chunks 0, 1; chunks 2, 3
+      uint64_t* full = &s->kv_full[stage][half];
+      if (!lat_wait(&s->kv_empty[stage][half], free_phase, abort_flag)) return false;
+      mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
+#pragma unroll 1
+      for (int i = 0, at = 0; i < pieces; ++i, at += step) {
+        const int4 rows = s->rows[ahead][i];
+        if (rows.x < 0) continue;
+        uint8_t* c0 = dst + 2 * half * kLatChunk + at * 128;
+        uint8_t* rot = dst + 4 * kLatChunk + at * 64;
+        if (run) {
+          if (half == 0) tma_load_2d(rot, tm_rot, full, 512, rows.x);
+          tma_load_2d(c0, tm_lat, full, half * 256, rows.x);
+          tma_load_2d(c0 + kLatChunk, tm_lat, full, half * 256 + 128, rows.x);
+        } else {
+          if (half == 0) tma_gather4(rot, tm_rot, full, 512, rows);
+          tma_gather4(c0, tm_lat, full, half * 256, rows);
+          tma_gather4(c0 + kLatChunk, tm_lat, full, half * 256 + 128, rows);
+        }
       }
     }
+    mbar_arrive(&s->tab_empty[ahead]);
   }
 }
 
@@ -562,13 +817,14 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   typename SM::Info* s = reinterpret_cast<typename SM::Info*>(smem + SM::kOffInfo);
   volatile int* abort_flag = &s->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kGroups = HG / 16;
+  constexpr int kGroups = SM::kGroups;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kLatStages; ++i) {
-      mbar_init(&s->kv_full[i], 1);
-      mbar_init(&s->kv_empty[i], 1);
-    }
+    for (int i = 0; i < kLatStages; ++i)
+      for (int c = 0; c < 2; ++c) {
+        mbar_init(&s->kv_full[i][c], 1);
+        mbar_init(&s->kv_empty[i][c], 1);
+      }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->s_empty[i], 4 * kGroups);
@@ -577,15 +833,18 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
       mbar_init(&s->frag_full[i], 1);
       mbar_init(&s->frag_empty[i], 2 + 4 * kGroups);
     }
+    for (int g = 0; g < kGroups; ++g) s->flag[g][0] = s->flag[g][1] = s->flag[g][2] = 0;
+    for (int i = 0; i < kLatAhead; ++i) {
+      mbar_init(&s->tab_full[i], 1);
+      mbar_init(&s->tab_empty[i], 1 + 4 * kGroups);
+    }
     mbar_init(&s->q_full, kGroups);
     s->abort = 0;
-    s->start_b = 0;
-    s->start_off = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_lat);
     prefetch_tensormap(&tm_rot);
   }
-  if (warp == 1) {
+  if (warp == 2) {
     tmem_alloc(&s->tmem, SM::kTmemCols);
     tmem_relinquish();
   }
@@ -594,8 +853,9 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   const int per = (a.table.B + SM::kThreads - 1) / SM::kThreads;
   const int b0 = threadIdx.x * per, b1 = min(a.table.B, b0 + per);
   long long mine = 0;
+  LatShape sh{};
   for (int b = b0; b < b1; ++b) {
-    const LatShape sh = lat_shape(a, b, HG);
+    sh = lat_shape(a, b, HG);
     mine += static_cast<long long>(sh.groups) * sh.tiles;
   }
   long long incl = mine;
@@ -612,19 +872,20 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     if (w < warp) before += s->scan[w];
     total += s->scan[w];
   }
-  const int gang_id = blockIdx.x / a.gang, rank = blockIdx.x % a.gang;
-  const int ngangs = static_cast<int>(min(static_cast<long long>(gridDim.x / a.gang), total));
+  const int gang_id = blockIdx.x >> a.gang_log, rank = blockIdx.x - (gang_id << a.gang_log);
+  const int ngangs = static_cast<int>(min(static_cast<long long>(gridDim.x >> a.gang_log), total));
   const bool works = gang_id < ngangs;
   if (works) {
-    const long long p0 = total * gang_id / ngangs;
+    const long long p0 = div_small(total * gang_id, ngangs);
     if (p0 >= before && p0 < before + mine) {
       long long off = before;
       for (int b = b0; b < b1; ++b) {
-        const LatShape sh = lat_shape(a, b, HG);
+        if (per > 1) sh = lat_shape(a, b, HG);
         const long long w = static_cast<long long>(sh.groups) * sh.tiles;
         if (p0 < off + w) {
           s->start_b = b;
           s->start_off = off;
+          s->start = sh;
           break;
         }
         off += w;
@@ -632,9 +893,9 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     }
   }
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = s->tmem;
   bool ok = true;
-
   if (!works) {
     if (threadIdx.x == 0) a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp >= 4) {
@@ -642,165 +903,18 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   } else if (warp == 2) {
     if (lane == 0) ok = lat_schedule<HG>(a, s, total, ngangs, gang_id, rank);
     __syncwarp();
-  } else if (warp == 0) {
-    // ------------------------------------------------------------ rows and scales
-    int it = 0, fslot = 0;
-    uint32_t fphase = 0;
-    const int ps = a.table.page_size, run = a.run;
-    for (;;) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&s->frag_full[fslot], fphase, abort_flag));
-      if (!ok) break;
-      const LatFragment f = s->frag[fslot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s->frag_empty[fslot]);
-      if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
-      if (!f.valid) break;
-      for (int tile = f.tile0; tile < f.tile1; ++tile, ++it) {
-        const int stage = it % kLatStages;
-        const int tok = tile * kLatTile;
-        // this lane's rows (a run of them, or four) and their scales, before the stage is free
-        int4 rows = make_int4(0, 0, 0, 0);
-        float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        bool live;
-        if (run) {
-          const int pos = tok + lane * run;
-          live = lane < kLatTile / run && pos < f.len;
-          float one = 0.0f;
-          if (live) {
-            const int page = table_page(a.table, f.first + pos / ps);
-            live = page >= 0;
-            if (live) {
-              rows.x = page * ps + pos % ps;
-              one = __ldg(a.scale + page);
-            }
-          }
-          one = __shfl_sync(0xffffffffu, one, 4 * lane / run);
-          sc = make_float4(one, one, one, one);
-        } else {
-          const int pos = tok + 4 * lane;
-          live = pos < f.len;
-          int* r = reinterpret_cast<int*>(&rows);
-          float* c = reinterpret_cast<float*>(&sc);
-          int fallback = -1;                               // a row past the end repeats one before it
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int p = min(pos + i, f.len - 1);
-            if (live) {
-              const int page = table_page(a.table, f.first + p / ps);
-              if (page >= 0) {
-                fallback = page * ps + p % ps;
-                c[i] = __ldg(a.scale + page);
-              }
-              r[i] = fallback;
-            }
-          }
-          if (live && fallback < 0) live = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (r[i] < 0) r[i] = max(fallback, 0);
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&s->kv_empty[stage], ((it / kLatStages) & 1) ^ 1u, abort_flag));
-        if (!ok) break;
-        *reinterpret_cast<float4*>(&s->scale[stage][4 * lane]) = sc;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * (run ? run : 4) * kLatDk;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&s->kv_full[stage], bytes);
-        __syncwarp();
-        if (live) {
-          uint8_t* dst = smem + stage * kLatStageBytes;
-          const int at = lane * (run ? run : 4);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (run) tma_load_2d(dst + c * kLatChunk + at * 128, &tm_lat, &s->kv_full[stage], c * 128, rows.x);
-            else tma_gather4(dst + c * kLatChunk + at * 128, &tm_lat, &s->kv_full[stage], c * 128, rows);
-          }
-          if (run) tma_load_2d(dst + 4 * kLatChunk + at * 64, &tm_rot, &s->kv_full[stage], 512, rows.x);
-          else tma_gather4(dst + 4 * kLatChunk + at * 64, &tm_rot, &s->kv_full[stage], 512, rows);
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-    }
+  } else if (warp == 1) {
+    ok = lat_mma_role<HG>(s, smem, tmem);
+  } else if (warp == 3) {
+    ok = lat_table_role<HG>(a, s);
+  } else {
+    if (lane == 0) ok = lat_load_role<HG>(a, &tm_lat, &tm_rot, s, smem);
+    __syncwarp();
     if (!ok) {
       // copies already in flight must land before the CTA's shared memory goes away
       const unsigned long long t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 10000000ull) {}
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = umma_idesc_e4m3_f32(128, SM::kQRows);
-      constexpr uint32_t kIdescO = umma_idesc_e4m3_f32(128, SM::kPRows) | (1u << 15) | (1u << 16);   // A and B M/N-major
-      const uint32_t base = smem_u32(smem);
-      int it0 = 0, fslot = 0, fcount = 0;
-      uint32_t fphase = 0;
-      while (ok) {
-        ok = mbar_wait(&s->frag_full[fslot], fphase, abort_flag);
-        if (!ok) break;
-        const int n = s->frag[fslot].tile1 - s->frag[fslot].tile0;
-        const bool valid = s->frag[fslot].valid != 0;
-        mbar_arrive(&s->frag_empty[fslot]);
-        if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
-        if (!valid) break;
-        ok = mbar_wait(&s->q_full, fcount & 1, abort_flag);
-        ++fcount;
-        if (!ok) break;
-        int qk = 0, pv = 0;
-        unsigned long long t0 = global_timer_ns();
-        for (uint32_t spin = 0; pv < n; ++spin) {
-          bool moved = false;
-          if (qk < n && qk <= pv + 1) {
-            const int i = it0 + qk, stage = i % kLatStages, buf = i & 1;
-            if (mbar_test(&s->kv_full[stage], (i / kLatStages) & 1) &&
-                mbar_test(&s->s_empty[buf], ((i >> 1) & 1) ^ 1u)) {
-              tc_fence_after();
-              const uint32_t kv = base + stage * kLatStageBytes, q = base + SM::kOffQ;
-              const uint32_t d = tmem + SM::kTmemS + buf * SM::kQRows;
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_f8(d, umma_desc(kv + c * kLatChunk + k * 32, 16, 1024, 2),
-                          umma_desc(q + (c * 8 + k * 2) * (SM::kQRows * 16), SM::kQRows * 16, 128, 0), kIdescS,
-                          (c | k) > 0 ? 1u : 0u);
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                umma_f8(d, umma_desc(kv + 4 * kLatChunk + k * 32, 16, 512, 4),
-                        umma_desc(q + (32 + k * 2) * (SM::kQRows * 16), SM::kQRows * 16, 128, 0), kIdescS, 1u);
-              umma_commit(&s->s_full[buf]);
-              ++qk;
-              moved = true;
-            }
-          }
-          if (pv < qk) {
-            const int i = it0 + pv, stage = i % kLatStages, buf = i & 1;
-            if (mbar_test(&s->p_full[buf], (i >> 1) & 1)) {
-              tc_fence_after();
-              const uint32_t kv = base + stage * kLatStageBytes, p = base + SM::kOffP + buf * SM::kPBytes;
-#pragma unroll 1
-              for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_f8(tmem + SM::kTmemO + m * SM::kPRows,
-                          umma_desc(kv + m * kLatChunk + k * 32 * 128, 1024, 1024, 2),
-                          umma_desc(p + k * 32 * 16, 128, 16 * kLatTile, 0), kIdescO, (pv | k) > 0 ? 1u : 0u);
-              umma_commit(&s->kv_empty[stage]);
-              umma_commit(&s->p_empty[buf]);
-              ++pv;
-              moved = true;
-            }
-          }
-          if (moved) {
-            t0 = global_timer_ns();
-          } else if ((spin & 63u) == 63u && (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
-        }
-        it0 += n;
-      }
-    }
-    __syncwarp();
   }
   if (!ok) {
     if (!*abort_flag) raise_device_error(FP8MOE_DEVERR_TIMEOUT);
@@ -808,46 +922,52 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, SM::kTmemCols);
   }
 }
 
-// Joins the parts of the column groups that were cut: one block per (CTA that holds a first
-// part, column), four value columns per thread; parts in order, so the same bits every time.
+// Joins the parts of the column groups that were cut: a warp per (CTA that holds a first part,
+// column), 16 value columns per lane; parts in order, so the same bits every time. A part holds
+// sums of 2^(score + m) and of those times values.
 template <int HG>
 __global__ void __launch_bounds__(128) mla_fp8_join_kernel(const LatAttnArgs a) {
-  const int cta = blockIdx.x, c = blockIdx.y;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
+  const int cta = blockIdx.x, c = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int4 job = a.merge[cta];
   if (job.z == 0 || c >= job.y) return;
-  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? job.w : 2 * (cta + i * a.gang)) * HG + c; };
-  float top = -INFINITY;
-  for (int i = 0; i < job.z; ++i) {
-    const float2 ml = a.part_ml[slot(i)];
-    if (ml.y != 0.0f) top = fmaxf(top, ml.x);              // (a NaN sum has a reference too)
-  }
-  if (top == -INFINITY) top = 0.0f;
-  float l = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? job.w : 2 * (cta + (i << a.gang_log))) * HG + c; };
+  float m = INFINITY;                                      // the part with the largest reference
+  for (int i = 0; i < job.z; ++i) m = fminf(m, a.part_ml[slot(i)].x);
+  if (m == INFINITY) m = 0.0f;
+  float l = 0.0f, acc[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
   for (int i = 0; i < job.z; ++i) {
     const size_t at = slot(i);
     const float2 ml = a.part_ml[at];
     if (ml.y == 0.0f) continue;
-    const float w = exp2f((ml.x == -INFINITY ? 0.0f : ml.x) - top);
-    const float4 x = reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[threadIdx.x];
+    const float w = exp2f(m - (ml.x == INFINITY ? 0.0f : ml.x));
     l += w * ml.y;
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[j * 32 + lane];
+      acc[4 * j] += w * x.x;
+      acc[4 * j + 1] += w * x.y;
+      acc[4 * j + 2] += w * x.z;
+      acc[4 * j + 3] += w * x.w;
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t row = static_cast<size_t>(job.x) + c;
-  __align__(8) __nv_bfloat162 y[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv),
-                                      __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
-  reinterpret_cast<uint2*>(a.o + row * kLatDv)[threadIdx.x] = *reinterpret_cast<const uint2*>(y);
-  if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.0f ? -INFINITY : (top - kLatPExp + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    __align__(8) __nv_bfloat162 y[2] = {__floats2bfloat162_rn(acc[4 * j] * inv, acc[4 * j + 1] * inv),
+                                        __floats2bfloat162_rn(acc[4 * j + 2] * inv, acc[4 * j + 3] * inv)};
+    reinterpret_cast<uint2*>(a.o + row * kLatDv)[j * 32 + lane] = *reinterpret_cast<const uint2*>(y);
+  }
+  if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : (log2f(l) - m) * 0.6931471805599453f;
 }
 
 }  // namespace fp8moe

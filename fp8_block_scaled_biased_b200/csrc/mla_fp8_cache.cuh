@@ -31,7 +31,7 @@ struct PageTable {
 // First page-table entry and token count of sequence b; false (and flagged) if the table's
 // entries for it are out of range. An empty sequence is a valid one of 0 tokens.
 __device__ __forceinline__ bool sequence_extent(const PageTable& t, int b, int& first, int& len) {
-  const int lo = __ldg(t.indptr + b), hi = __ldg(t.indptr + b + 1);
+  const int lo = __ldg(t.indptr + b), hi = __ldg(t.indptr + b + 1), last = __ldg(t.last_lens + b);
   first = lo;
   len = 0;
   if (lo < 0 || hi < lo || hi > t.num_indices) {
@@ -39,7 +39,6 @@ __device__ __forceinline__ bool sequence_extent(const PageTable& t, int b, int& 
     return false;
   }
   if (hi == lo) return true;
-  const int last = __ldg(t.last_lens + b);
   if (last < 1 || last > t.page_size) {
     raise_device_error(FP8MOE_DEVERR_PAGE);
     return false;
