@@ -43,12 +43,13 @@ namespace fp8moe {
 
 constexpr int kLatDv = 512;
 constexpr int kLatTile = 128;                              // tokens per tile
-constexpr int kLatStages = 2;
 constexpr int kLatAhead = 4;                               // tiles whose page-table entries are fetched ahead
 constexpr int kLatChunk = kLatTile * 128;                  // 128 bytes of every row of a tile
-constexpr int kLatStageBytes = kLatTile * kLatDk;          // four chunks and the 64 rotary bytes
+constexpr int kLatHalf = 2 * kLatChunk;                    // two chunks: what is loaded and freed together
+constexpr int kLatRot = kLatTile * 64;                     // the rotary bytes of a tile
 constexpr int kLatMaxCtas = 148;                           // one per SM
 constexpr float kLatHeadroom = 4.0f;                       // a weight may pass its reference by 2^4
+constexpr float kLatNoRef = 1e30f;                         // reference of a column that has none: any score passes it
 constexpr float kLatPExp = 4.0f;                           // reference weight as a code: 2^4, at most 2^8 <= 448
 
 struct LatAttnArgs {
@@ -87,7 +88,12 @@ struct LatSmem {
   static constexpr int kQRows = 2 * HG, kPRows = 3 * HG;
   static constexpr int kQBytes = kQRows * kLatDk;
   static constexpr int kPBytes = kPRows * kLatTile;
-  static constexpr int kOffQ = kLatStages * kLatStageBytes;
+  // Halves of tiles in flight, as many as shared memory holds beside the queries and weights: with 16
+  // columns 2.5 tiles (an 8K decode batch took 78 us with 2), with 32 columns 2 tiles. Half 0 of a tile
+  // brings its rotary bytes along; they are free once the tile three (two) before has gone.
+  static constexpr int kHalves = HG == 16 ? 5 : 4, kRots = HG == 16 ? 3 : 2;
+  static constexpr int kOffRot = kHalves * kLatHalf;
+  static constexpr int kOffQ = kOffRot + kRots * kLatRot;
   static constexpr int kOffP = kOffQ + kQBytes;
   static constexpr int kOffInfo = kOffP + 2 * kPBytes;
   // TMEM columns: two score buffers, four accumulators of 128 value columns
@@ -103,7 +109,7 @@ struct LatSmem {
     int live[kLatAhead];          // rows to be loaded; -1: the end of the list
     uint64_t tab_full[kLatAhead], tab_empty[kLatAhead];
     float red[kGroups][4][8], inv[kGroups][8];
-    uint64_t kv_full[kLatStages][2], kv_empty[kLatStages][2];   // per half of a stage
+    uint64_t kv_full[kHalves], kv_empty[kHalves];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t frag_full[2], frag_empty[2], q_full;
     int flag[kGroups][3];         // a score passed its reference's bound (1), a wait failed (2); tiles take turns
@@ -116,6 +122,16 @@ struct LatSmem {
   };
   static constexpr int kBytes = kOffInfo + static_cast<int>(sizeof(Info)) + 1024;   // + alignment
 };
+
+// Position of a half of a tile in the ring: its slot, and the parity of the slot's use.
+struct LatHalf {
+  int slot;
+  uint32_t phase;
+};
+template <int N>
+__device__ __forceinline__ LatHalf lat_half(int n) {
+  return {n % N, static_cast<uint32_t>(n / N) & 1u};
+}
 
 // ---------------------------------------------------------------- PTX
 __device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int4 rows) {
@@ -339,8 +355,7 @@ __device__ __forceinline__ float pick8(const float (&v)[8], int i) {
 // each) and stores them as the score MMAs' B operand: core matrices of 8 rows x 16 bytes, rows
 // 16 g .. 16 g + 7 the high terms, the next 8 the low ones. Returns the scale of column tid / 16:
 // NaN for a row with an entry that is not finite, which makes all its scores NaN whatever its codes
-// are. (The second pass reads L1 again: registers cannot be indexed in a loop, and unrolled code
-// costs more in instruction fetches than it saves.)
+// are.
 template <int HG>
 __device__ __forceinline__ float lat_load_queries(const LatAttnArgs& a, const LatFragment& f, uint8_t* qs, int group,
                                                   int tid) {
@@ -349,13 +364,11 @@ __device__ __forceinline__ float lat_load_queries(const LatAttnArgs& a, const La
   const bool live = c < f.cols;
   const uint2* src = reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(f.row0) + (live ? c : 0)) * kLatDk) + part;
   uint32_t mx = 0;
-  {
-    uint2 x[9];
+  uint2 x[9];
 #pragma unroll
-    for (int j = 0; j < 9; ++j) x[j] = __ldg(src + 16 * j);
+  for (int j = 0; j < 9; ++j) x[j] = __ldg(src + 16 * j);
 #pragma unroll
-    for (int j = 0; j < 9; ++j) mx = __vmaxu2(mx, __vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu));
-  }
+  for (int j = 0; j < 9; ++j) mx = __vmaxu2(mx, __vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu));
   mx = max(mx & 0xffffu, mx >> 16);
   for (int d = 1; d < 16; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   if (!live) mx = 0;
@@ -363,11 +376,9 @@ __device__ __forceinline__ float lat_load_queries(const LatAttnArgs& a, const La
   const float inv = live ? __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.0f;
   const __half2 k16 = __float2half2_rn(16.0f);
   uint8_t* dst = qs + (part >> 2) * (SM::kQRows * 16) + (part & 3) * 4 + (group * 16 + (tid >> 4)) * 16;
-  uint2 x = __ldg(src);
-#pragma unroll 1
+#pragma unroll
   for (int j = 0; j < 9; ++j) {
-    const float2 v0 = bf16x2_to_float(x.x), v1 = bf16x2_to_float(x.y);
-    if (j < 8) x = __ldg(src + 16 * (j + 1));
+    const float2 v0 = bf16x2_to_float(x[j].x), v1 = bf16x2_to_float(x[j].y);
     const __half2 h0 = __floats2half2_rn(v0.x * inv, v0.y * inv), h1 = __floats2half2_rn(v1.x * inv, v1.y * inv);
     const uint16_t hi0 = half2_to_e4m3x2(h0), hi1 = half2_to_e4m3x2(h1);           // at most 448: h exact above 2^-16
     const uint16_t lo0 = half2_to_e4m3x2(__hmul2(__hsub2(h0, e4m3x2_to_half2(hi0)), k16));
@@ -422,7 +433,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       fac[c] = s->inv[group][c];
-      nref[c] = INFINITY;
+      nref[c] = kLatNoRef;
       sum[c] = 0.0f;
     }
     const int query = (f.col0 + group * 8) / a.Hq;
@@ -430,7 +441,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     const int next_query = (query + 1) * a.Hq - (f.col0 + group * 8);  // columns until the next query
 
     for (int tile = f.tile0; tile < f.tile1; ++tile, ++it, turn = turn == 2 ? 0 : turn + 1) {
-      const int buf = it & 1, stage = it % kLatStages;
+      const int buf = it & 1;
       const uint32_t phase = (it >> 1) & 1;
       const int ahead = it % kLatAhead;
       ok = lat_wait(&s->tab_full[ahead], (it / kLatAhead) & 1, abort_flag);
@@ -439,9 +450,9 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       if (lane == 0) mbar_arrive(&s->tab_empty[ahead]);
       // the reference of a column bounds score + log2(page scale): the weights that meet the codes
       const float bound = kLatPExp + kLatHeadroom - (sc > 0.0f ? __log2f(sc) : -100.0f);
-      float fs[8];
+      float2 fs[4];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) fs[c] = fac[c] * sc;
+      for (int i = 0; i < 4; ++i) fs[i] = make_float2(fac[2 * i] * sc, fac[2 * i + 1] * sc);
       ok = lat_wait(&s->s_full[buf], phase, abort_flag) && ok;
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
@@ -452,7 +463,13 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
         tc_fence_before();
         if (lane == 0) mbar_arrive(&s->s_empty[buf]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) t[c] = fmaf(v[8 + c], 0.0625f, v[c]) * fs[c];
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = __fmul2_rn(__ffma2_rn(make_float2(v[8 + 2 * i], v[9 + 2 * i]), make_float2(0.0625f, 0.0625f),
+                                                 make_float2(v[2 * i], v[2 * i + 1])),
+                                      fs[i]);
+          t[2 * i] = x.x;
+          t[2 * i + 1] = x.y;
+        }
       }
       bool bad = false;                                    // a NaN in this token's row: every score is NaN
       if (isnan(t[0])) {
@@ -479,7 +496,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         w[c] = t[c] + nref[c];
-        top = fmaxf(top, t[c] == -INFINITY ? -INFINITY : w[c]);
+        top = fmaxf(top, w[c]);
       }
       // A raised flag is read after the barrier below; until then the weights are computed as if there
       // were none.
@@ -488,7 +505,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       uint32_t hi[2], lo[2], lo2[2];
       for (bool again = false;; again = true) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = exp2_fast(t[c] == -INFINITY ? -INFINITY : w[c]);
+        for (int c = 0; c < 8; ++c) w[c] = exp2_fast(w[c]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint16_t h[2], l[2], l2[2];
@@ -521,7 +538,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
           const float m = fmaxf(fmaxf(s->red[group][0][c], s->red[group][1][c]),
                                 fmaxf(s->red[group][2][c], s->red[group][3][c]));
           const float next = fminf(nref[c], kLatPExp - m); // m = -inf: as it was
-          alpha[c] = next == INFINITY ? 1.0f : exp2_fast(next - nref[c]);
+          alpha[c] = exp2_fast(next - nref[c]);
           nref[c] = next;
           sum[c] *= alpha[c];
           w[c] = t[c] + next;
@@ -549,10 +566,10 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       if (bad) {
         // the row must not reach columns that give it no weight (0 x NaN): its values become 0, the
         // weights of the columns that do see it are NaN themselves
-        uint8_t* row = smem + stage * kLatStageBytes + tid * 128;
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
-          *reinterpret_cast<uint4*>(row + (i >> 3) * kLatChunk + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(smem + lat_half<SM::kHalves>(2 * it + (i >> 4)).slot * kLatHalf +
+                                    ((i >> 3) & 1) * kLatChunk + tid * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -586,7 +603,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       const float m = pick8(nref, tid);                    // l sums 2^(score + m)
       if (tid < live) {
         if (f.slot >= 0) a.part_ml[part0 + tid] = make_float2(m, l);
-        else if (a.lse) a.lse[row0 + tid] = l == 0.0f ? -INFINITY : (log2f(l) - (m == INFINITY ? 0.0f : m)) * kLn2;
+        else if (a.lse) a.lse[row0 + tid] = l == 0.0f ? -INFINITY : (log2f(l) - m) * kLn2;
       }
       // what the accumulators are multiplied by: a part stays as it is
       s->inv[group][tid] = f.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
@@ -628,7 +645,7 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
   const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   const uint64_t desc_k = umma_desc(base, 16, 1024, 2);                            // rows of 128 bytes, K-major
-  const uint64_t desc_rot = umma_desc(base + 4 * kLatChunk, 16, 512, 4);           // rows of 64 bytes
+  const uint64_t desc_rot = umma_desc(base + SM::kOffRot, 16, 512, 4);             // rows of 64 bytes
   const uint64_t desc_q = umma_desc(base + SM::kOffQ, SM::kQRows * 16, 128, 0);
   const uint64_t desc_v = umma_desc(base, 1024, 1024, 2);                          // the same rows, M-major
   const uint64_t desc_p = umma_desc(base + SM::kOffP, 128, 16 * kLatTile, 0);
@@ -646,26 +663,28 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
     int qk = 0, pv = 0;
     unsigned long long t0 = 0;
     for (uint32_t spin = 0; pv < n; ++spin) {
-      const int i = it0 + qk, stage = i % kLatStages, buf = i & 1;
-      const int j = it0 + pv, pstage = j % kLatStages, pbuf = j & 1;
-      uint64_t* bar = lane < 2 ? &s->kv_full[stage][lane] : lane == 2 ? &s->s_empty[buf] : &s->p_full[pbuf];
-      const uint32_t parity = lane < 2 ? (i / kLatStages) & 1 : lane == 2 ? ((i >> 1) & 1) ^ 1u : (j >> 1) & 1;
+      const int i = it0 + qk, buf = i & 1;
+      const int j = it0 + pv, pbuf = j & 1;
+      const LatHalf mine = lat_half<SM::kHalves>(2 * i + (lane & 1));
+      uint64_t* bar = lane < 2 ? &s->kv_full[mine.slot] : lane == 2 ? &s->s_empty[buf] : &s->p_full[pbuf];
+      const uint32_t parity = lane < 2 ? mine.phase : lane == 2 ? ((i >> 1) & 1) ^ 1u : (j >> 1) & 1;
       const uint32_t ready = __ballot_sync(0xffffffffu, mbar_test(bar, parity));
       const bool do_qk = qk < n && qk <= pv + 1 && (ready & 7u) == 7u;
       const bool do_pv = pv < qk && (ready & 8u) != 0;
       if (do_qk || do_pv) tc_fence_after();
       if (do_pv) {
         if (leader) {
-          const uint64_t kv = static_cast<uint64_t>(pstage * kLatStageBytes) >> 4;
+          const int h0 = lat_half<SM::kHalves>(2 * j).slot, h1 = lat_half<SM::kHalves>(2 * j + 1).slot;
           const uint64_t p = desc_p + (pbuf * (SM::kPBytes >> 4));
           const uint32_t more = pv > 0 ? 1u : 0u;
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_f8(tmem + SM::kTmemO + m * SM::kPRows, desc_v + kv + m * (kLatChunk >> 4) + k * 256, p + k * 32,
+              umma_f8(tmem + SM::kTmemO + m * SM::kPRows,
+                      desc_v + (m < 2 ? h0 : h1) * (kLatHalf >> 4) + (m & 1) * (kLatChunk >> 4) + k * 256, p + k * 32,
                       kIdescO, k > 0 ? 1u : more);
-            if (m & 1) umma_commit(&s->kv_empty[pstage][m >> 1]);
+            if (m & 1) umma_commit(&s->kv_empty[m < 2 ? h0 : h1]);
           }
           umma_commit(&s->p_empty[pbuf]);
         }
@@ -675,16 +694,17 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
       }
       if (do_qk) {
         if (leader) {
-          const uint64_t kv = static_cast<uint64_t>(stage * kLatStageBytes) >> 4;
+          const int h0 = lat_half<SM::kHalves>(2 * i).slot, h1 = lat_half<SM::kHalves>(2 * i + 1).slot;
+          const uint64_t rot = static_cast<uint64_t>(i % SM::kRots * kLatRot) >> 4;
           const uint32_t d = tmem + SM::kTmemS + buf * SM::kQRows;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            umma_f8(d, desc_rot + kv + k * 2, desc_q + (32 + k * 2) * SM::kQRows, kIdescS, k > 0 ? 1u : 0u);
+            umma_f8(d, desc_rot + rot + k * 2, desc_q + (32 + k * 2) * SM::kQRows, kIdescS, k > 0 ? 1u : 0u);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_f8(d, desc_k + kv + c * (kLatChunk >> 4) + k * 2, desc_q + (c * 8 + k * 2) * SM::kQRows, kIdescS, 1u);
+              umma_f8(d, desc_k + (c < 2 ? h0 : h1) * (kLatHalf >> 4) + (c & 1) * (kLatChunk >> 4) + k * 2, desc_q + (c * 8 + k * 2) * SM::kQRows, kIdescS, 1u);
           umma_commit(&s->s_full[buf]);
         }
         __syncwarp();
@@ -767,38 +787,50 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
   }
 }
 
-// Warp 0, one thread: the loads, a half of a stage at a time as P V frees them.
+// Warp 0, one thread: the loads, a half of a tile at a time as P V frees them.
 template <int HG>
 __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtensorMap* tm_lat, const CUtensorMap* tm_rot,
                                               typename LatSmem<HG>::Info* s, uint8_t* smem) {
+  using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
   const int run = a.run, step = run ? run : 4, pieces = kLatTile / step;
   for (int it = 0;; ++it) {
-    const int stage = it % kLatStages, ahead = it % kLatAhead;
-    const uint32_t free_phase = ((it / kLatStages) & 1) ^ 1u;
+    const int ahead = it % kLatAhead;
     if (!lat_wait(&s->tab_full[ahead], (it / kLatAhead) & 1, abort_flag)) return false;
     const int live = s->live[ahead];
     if (live < 0) return true;
-    uint8_t* dst = smem + stage * kLatStageBytes;
+    int4 first[2] = {s->rows[ahead][0], s->rows[ahead][1]};            // pages of 64 and more need no others
+    uint8_t* rot = smem + SM::kOffRot + it % SM::kRots * kLatRot;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {                 // rotary entries and chunks 0, 1; chunks 2, 3
-      uint64_t* full = &s->kv_full[stage][half];
-      if (!lat_wait(&s->kv_empty[stage][half], free_phase, abort_flag)) return false;
+      const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
+      uint64_t* full = &s->kv_full[h.slot];
+      uint8_t* dst = smem + h.slot * kLatHalf;
+      if (!lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag)) return false;
       mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
+      if (run >= 64) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i < pieces && first[i].x >= 0) {
+            if (half == 0) tma_load_2d(rot + i * 64 * 64, tm_rot, full, 512, first[i].x);
+            tma_load_2d(dst + i * 64 * 128, tm_lat, full, half * 256, first[i].x);
+            tma_load_2d(dst + kLatChunk + i * 64 * 128, tm_lat, full, half * 256 + 128, first[i].x);
+          }
+        }
+      } else {
 #pragma unroll 1
-      for (int i = 0, at = 0; i < pieces; ++i, at += step) {
-        const int4 rows = s->rows[ahead][i];
-        if (rows.x < 0) continue;
-        uint8_t* c0 = dst + 2 * half * kLatChunk + at * 128;
-        uint8_t* rot = dst + 4 * kLatChunk + at * 64;
-        if (run) {
-          if (half == 0) tma_load_2d(rot, tm_rot, full, 512, rows.x);
-          tma_load_2d(c0, tm_lat, full, half * 256, rows.x);
-          tma_load_2d(c0 + kLatChunk, tm_lat, full, half * 256 + 128, rows.x);
-        } else {
-          if (half == 0) tma_gather4(rot, tm_rot, full, 512, rows);
-          tma_gather4(c0, tm_lat, full, half * 256, rows);
-          tma_gather4(c0 + kLatChunk, tm_lat, full, half * 256 + 128, rows);
+        for (int i = 0, at = 0; i < pieces; ++i, at += step) {
+          const int4 rows = s->rows[ahead][i];
+          if (rows.x < 0) continue;
+          if (run) {
+            if (half == 0) tma_load_2d(rot + at * 64, tm_rot, full, 512, rows.x);
+            tma_load_2d(dst + at * 128, tm_lat, full, half * 256, rows.x);
+            tma_load_2d(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, rows.x);
+          } else {
+            if (half == 0) tma_gather4(rot + at * 64, tm_rot, full, 512, rows);
+            tma_gather4(dst + at * 128, tm_lat, full, half * 256, rows);
+            tma_gather4(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, rows);
+          }
         }
       }
     }
@@ -820,11 +852,10 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   constexpr int kGroups = SM::kGroups;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kLatStages; ++i)
-      for (int c = 0; c < 2; ++c) {
-        mbar_init(&s->kv_full[i][c], 1);
-        mbar_init(&s->kv_empty[i][c], 1);
-      }
+    for (int i = 0; i < SM::kHalves; ++i) {
+      mbar_init(&s->kv_full[i], 1);
+      mbar_init(&s->kv_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->s_empty[i], 4 * kGroups);
@@ -940,7 +971,6 @@ __global__ void __launch_bounds__(128) mla_fp8_join_kernel(const LatAttnArgs a) 
   auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? job.w : 2 * (cta + (i << a.gang_log))) * HG + c; };
   float m = INFINITY;                                      // the part with the largest reference
   for (int i = 0; i < job.z; ++i) m = fminf(m, a.part_ml[slot(i)].x);
-  if (m == INFINITY) m = 0.0f;
   float l = 0.0f, acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
@@ -948,7 +978,7 @@ __global__ void __launch_bounds__(128) mla_fp8_join_kernel(const LatAttnArgs a) 
     const size_t at = slot(i);
     const float2 ml = a.part_ml[at];
     if (ml.y == 0.0f) continue;
-    const float w = exp2f(m - (ml.x == INFINITY ? 0.0f : ml.x));
+    const float w = exp2f(m - ml.x);
     l += w * ml.y;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
