@@ -25,7 +25,7 @@
 //   warp 1      the MMAs: scores of the next tile are issued ahead of this tile's P V if its
 //               rows have landed, else after
 //   warp 2      the work list (below), TMEM
-//   warps 4..   one warpgroup per 8 columns, a token per thread: online softmax. The running
+//   warps 4-11  two warpgroups, half of the columns each, a token per thread: online softmax. The running
 //               reference of a column only moves when a score passes it by more than one
 //               (base 2), and then the accumulators in TMEM are rescaled.
 //
@@ -48,9 +48,14 @@ constexpr int kLatChunk = kLatTile * 128;                  // 128 bytes of every
 constexpr int kLatHalf = 2 * kLatChunk;                    // two chunks: what is loaded and freed together
 constexpr int kLatRot = kLatTile * 64;                     // the rotary bytes of a tile
 constexpr int kLatMaxCtas = 148;                           // one per SM
-constexpr float kLatHeadroom = 4.0f;                       // a weight may pass its reference by 2^4
+// A weight's code runs up to 2^8 (of 448). Its column's reference stands at 2^2, so a score may pass the
+// reference by 6 (base 2) before it has to move, which happens in about one tile of a hundred (of five,
+// with 4); what falls below 2^-22 of the reference is lost, at most a half of its size and at most
+// 2^-22 each. Longer contexts, whose references settle early on, get a higher reference, so that all
+// their tokens together lose less than 2^-8: half a step of the bf16 output.
+__device__ __forceinline__ float lat_ref_exponent(int len) { return len <= (1 << 14) ? 2.0f : len <= (1 << 16) ? 4.0f : 6.0f; }
+constexpr float kLatTopExp = 8.0f;
 constexpr float kLatNoRef = 1e30f;                         // reference of a column that has none: any score passes it
-constexpr float kLatPExp = 4.0f;                           // reference weight as a code: 2^4, at most 2^8 <= 448
 
 struct LatAttnArgs {
   const __nv_bfloat16* q;        // [num_q, Hq, 576]
@@ -99,7 +104,7 @@ struct LatSmem {
   // TMEM columns: two score buffers, four accumulators of 128 value columns
   static constexpr int kTmemS = 0, kTmemO = 2 * kQRows;
   static constexpr int kTmemCols = (kTmemO + 4 * kPRows <= 256) ? 256 : 512;
-  static constexpr int kGroups = HG / 8;                   // softmax warpgroups
+  static constexpr int kGroups = HG / 8, kCols = 8;   // softmax warpgroups, columns of each
   static constexpr int kThreads = 128 + 128 * kGroups;
   struct Info {
     LatFragment frag[2];
@@ -108,7 +113,7 @@ struct LatSmem {
     float scale[kLatAhead][kLatTile];
     int live[kLatAhead];          // rows to be loaded; -1: the end of the list
     uint64_t tab_full[kLatAhead], tab_empty[kLatAhead];
-    float red[kGroups][4][8], inv[kGroups][8];
+    float red[kGroups][4][kCols], inv[kGroups][kCols];
     uint64_t kv_full[kHalves], kv_empty[kHalves];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t frag_full[2], frag_empty[2], q_full;
@@ -142,18 +147,29 @@ __device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* m
       "r"(rows.w)
       : "memory");
 }
-// 32 lanes x 16 consecutive fp32 columns, waited for.
-__device__ __forceinline__ void tmem_load_16(uint32_t taddr, float (&v)[16]) {
+// 32 lanes x consecutive fp32 columns (in one or two runs): loads are waited for once, stores are not.
+__device__ __forceinline__ void tmem_load_16(uint32_t at0, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-      : "r"(taddr)
+      : "r"(at0)
       : "memory");
 }
-// 16 columns and 8 more elsewhere, waited for once.
-__device__ __forceinline__ void tmem_load_16_8(uint32_t at16, uint32_t at8, float (&v)[24]) {
+__device__ __forceinline__ void tmem_load_32(uint32_t at0, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(at0)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load_16_8(uint32_t at0, uint32_t at1, float (&v)[24]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%24];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%25];\n\t"
@@ -161,16 +177,46 @@ __device__ __forceinline__ void tmem_load_16_8(uint32_t at16, uint32_t at8, floa
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
         "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23])
-      : "r"(at16), "r"(at8)
+      : "r"(at0), "r"(at1)
       : "memory");
 }
-__device__ __forceinline__ void tmem_store_16_8(uint32_t at16, uint32_t at8, const float (&v)[24]) {
+__device__ __forceinline__ void tmem_load_32_16(uint32_t at0, uint32_t at1, float (&v)[48]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%48];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47},"
+      " [%49];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
+        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
+        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47])
+      : "r"(at0), "r"(at1)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_16_8(uint32_t at0, uint32_t at1, const float (&v)[24]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%24], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n\t"
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%25], {%16,%17,%18,%19,%20,%21,%22,%23};" ::"f"(v[0]),
-      "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
-      "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]),
-      "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "r"(at16), "r"(at8)
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%25], {%16,%17,%18,%19,%20,%21,%22,%23};"
+      ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
+        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
+        "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "r"(at0), "r"(at1)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_32_16(uint32_t at0, uint32_t at1, const float (&v)[48]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%48], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\t"
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%49], {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,"
+      "%46,%47};"
+      ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
+        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
+        "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]),
+        "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "f"(v[32]), "f"(v[33]), "f"(v[34]), "f"(v[35]),
+        "f"(v[36]), "f"(v[37]), "f"(v[38]), "f"(v[39]), "f"(v[40]), "f"(v[41]), "f"(v[42]), "f"(v[43]), "f"(v[44]),
+        "f"(v[45]), "f"(v[46]), "f"(v[47]), "r"(at0), "r"(at1)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -267,8 +313,7 @@ __device__ __noinline__ long long div_small(long long a, long long b) {
 // Warp 2, one lane: the fragments of positions [p0, p1) of the work list, through the ring.
 template <int HG>
 __device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatSmem<HG>::Info* s, long long total,
-                                             int ngangs, int gang_id, int rank) {
-  const long long p0 = div_small(total * gang_id, ngangs), p1 = div_small(total * (gang_id + 1), ngangs);
+                                             int ngangs, int gang_id, int rank, long long p0, long long p1) {
   int b = s->start_b;
   long long off = s->start_off;
   LatShape sh = s->start;
@@ -344,65 +389,98 @@ __device__ __forceinline__ int float_order(float x) {      // order of floats as
 __device__ __forceinline__ float order_float(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
 
 // One of a thread's columns chosen by a runtime index, without indexing registers.
-__device__ __forceinline__ float pick8(const float (&v)[8], int i) {
+template <int C>
+__device__ __forceinline__ float pick(const float (&v)[C], int i) {
   float x = v[0];
 #pragma unroll
-  for (int c = 1; c < 8; ++c) x = i == c ? v[c] : x;
+  for (int c = 1; c < C; ++c) x = i == c ? v[c] : x;
   return x;
 }
 
-// Splits this warpgroup's 8 query columns into their two terms (16 threads per column, 36 entries
-// each) and stores them as the score MMAs' B operand: core matrices of 8 rows x 16 bytes, rows
-// 16 g .. 16 g + 7 the high terms, the next 8 the low ones. Returns the scale of column tid / 16:
-// NaN for a row with an entry that is not finite, which makes all its scores NaN whatever its codes
-// are.
+// A thread's share of its warpgroup's query columns: 128 / C threads per column, 9 pieces of C / 2
+// bf16 entries each. Loaded while the fragment before is written out.
 template <int HG>
-__device__ __forceinline__ float lat_load_queries(const LatAttnArgs& a, const LatFragment& f, uint8_t* qs, int group,
-                                                  int tid) {
-  using SM = LatSmem<HG>;
-  const int c = group * 8 + (tid >> 4), part = tid & 15;
-  const bool live = c < f.cols;
-  const uint2* src = reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(f.row0) + (live ? c : 0)) * kLatDk) + part;
-  uint32_t mx = 0;
-  uint2 x[9];
+struct LatQueries {
+  static constexpr int C = LatSmem<HG>::kCols, kPer = 128 / C, kWords = C / 4;
+  uint32_t x[9][kWords];
+
+  __device__ __forceinline__ void load(const LatAttnArgs& a, const LatFragment& f, int group, int tid) {
+    const int c = group * C + tid / kPer;
+    // a column without a query repeats the fragment's first one: its result is not written
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        a.q + (static_cast<size_t>(f.row0) + (c < f.cols ? c : 0)) * kLatDk) + tid % kPer * kWords;
 #pragma unroll
-  for (int j = 0; j < 9; ++j) x[j] = __ldg(src + 16 * j);
-#pragma unroll
-  for (int j = 0; j < 9; ++j) mx = __vmaxu2(mx, __vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu));
-  mx = max(mx & 0xffffu, mx >> 16);
-  for (int d = 1; d < 16; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  if (!live) mx = 0;
-  const int ex = max(kScaleMinExp, static_cast<int>(mx >> 7) - 135 + ((mx & 0x7fu) > 96u ? 1 : 0));
-  const float inv = live ? __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.0f;
-  const __half2 k16 = __float2half2_rn(16.0f);
-  uint8_t* dst = qs + (part >> 2) * (SM::kQRows * 16) + (part & 3) * 4 + (group * 16 + (tid >> 4)) * 16;
-#pragma unroll
-  for (int j = 0; j < 9; ++j) {
-    const float2 v0 = bf16x2_to_float(x[j].x), v1 = bf16x2_to_float(x[j].y);
-    const __half2 h0 = __floats2half2_rn(v0.x * inv, v0.y * inv), h1 = __floats2half2_rn(v1.x * inv, v1.y * inv);
-    const uint16_t hi0 = half2_to_e4m3x2(h0), hi1 = half2_to_e4m3x2(h1);           // at most 448: h exact above 2^-16
-    const uint16_t lo0 = half2_to_e4m3x2(__hmul2(__hsub2(h0, e4m3x2_to_half2(hi0)), k16));
-    const uint16_t lo1 = half2_to_e4m3x2(__hmul2(__hsub2(h1, e4m3x2_to_half2(hi1)), k16));
-    *reinterpret_cast<uint32_t*>(dst) = hi0 | (static_cast<uint32_t>(hi1) << 16);
-    *reinterpret_cast<uint32_t*>(dst + 128) = lo0 | (static_cast<uint32_t>(lo1) << 16);
-    dst += 4 * (SM::kQRows * 16);                          // 64 entries on
+    for (int j = 0; j < 9; ++j) {
+      if constexpr (kWords == 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + j * kPer * 4));
+        x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + j * kPer * 2));
+        x[j][0] = v.x, x[j][1] = v.y;
+      }
+    }
   }
-  return mx >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-}
+
+  // Splits the entries into their two terms and stores them as the score MMAs' B operand: core
+  // matrices of 8 rows x 16 bytes, this group's rows being its C high terms, then its C low ones.
+  // Returns the scale of column tid / kPer: NaN for a row with an entry that is not finite, which makes
+  // all its scores NaN whatever its codes are.
+  __device__ __forceinline__ float store(uint8_t* qs, int group, int tid) const {
+    constexpr int kLead = LatSmem<HG>::kQRows * 16;        // from 16 entries to the next
+    uint32_t mx = 0;
+#pragma unroll
+    for (int j = 0; j < 9; ++j)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) mx = __vmaxu2(mx, x[j][i] & 0x7fff7fffu);
+    mx = max(mx & 0xffffu, mx >> 16);
+    for (int d = 1; d < kPer; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const int ex = max(kScaleMinExp, static_cast<int>(mx >> 7) - 135 + ((mx & 0x7fu) > 96u ? 1 : 0));
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+    const __half2 k16 = __float2half2_rn(16.0f);
+    const int at = tid % kPer * kWords * 2;                // this thread's entries of each kPer * C / 2
+    uint8_t* dst = qs + (at >> 4) * kLead + (at & 15) + (group * 2 * C + tid / kPer) * 16;
+#pragma unroll
+    for (int j = 0; j < 9; ++j, dst += 4 * kLead) {        // 64 entries on
+      uint32_t hi[kWords / 2], lo[kWords / 2];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const float2 v = bf16x2_to_float(x[j][i]);
+        const __half2 h = __floats2half2_rn(v.x * inv, v.y * inv);     // at most 448: exact above 2^-16
+        const uint32_t a = half2_to_e4m3x2(h);
+        const uint32_t b = half2_to_e4m3x2(__hmul2(__hsub2(h, e4m3x2_to_half2(static_cast<uint16_t>(a))), k16));
+        hi[i / 2] = i % 2 ? hi[i / 2] | a << 16 : a;
+        lo[i / 2] = i % 2 ? lo[i / 2] | b << 16 : b;
+      }
+      if constexpr (kWords == 4) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + C * 16) = make_uint2(lo[0], lo[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(dst) = hi[0];
+        *reinterpret_cast<uint32_t*>(dst + C * 16) = lo[0];
+      }
+    }
+    return mx >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+  }
+};
 
 template <int HG>
 __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename LatSmem<HG>::Info* s, uint8_t* smem,
                                                  uint32_t tmem) {
   using SM = LatSmem<HG>;
+  constexpr int C = SM::kCols;
   volatile int* abort_flag = &s->abort;
-  const int tid = threadIdx.x & 127, group = (threadIdx.x >> 7) - 1;   // warpgroup of 8 columns
+  const int tid = threadIdx.x & 127, group = (threadIdx.x >> 7) - 1;   // warpgroup of C columns
   const int warp = tid >> 5, lane = tid & 31;
   const int bar_id = 1 + group;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-  // The terms of two groups' weights share 48 N columns: hi and lo of the first, both lo2, hi and lo
-  // of the second; 16 bytes of a token's weights are one block of 16 N columns.
-  const int block = 3 * (group >> 1) + 2 * (group & 1), block2 = 3 * (group >> 1) + 1, half8 = 8 * (group & 1);
-  const uint32_t acc_hi = lane_base + SM::kTmemO + 16 * block, acc_lo2 = lane_base + SM::kTmemO + 16 * block2 + half8;
+  // N columns of the weights' terms, in blocks of 16: hi, lo, lo2 of each group of 16 columns; or, of two
+  // groups of 8, hi and lo of the first, both lo2, hi and lo of the second.
+  const int block = C == 16 ? 3 * group : 3 * (group >> 1) + 2 * (group & 1), block2 = C == 16 ? block + 2 : 3 * (group >> 1) + 1, at2 = C == 16 ? 0 : 8 * (group & 1);
+  const uint32_t acc1 = lane_base + SM::kTmemO + 16 * block, acc2 = lane_base + SM::kTmemO + 16 * block2 + at2;
+  auto load_acc = [&](int m, float (&x)[3 * C]) {          // hi, lo and lo2 sums of 128 value columns
+    if constexpr (C == 16) tmem_load_32_16(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
+    else tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
+  };
   const float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   const bool capped = a.logit_cap > 0.0f;
   // cap * tanh(t / cap) * log2(e) = cap2 - 2 cap2 / (1 + 2^(t cap_in)): off by a few 2^-24 of the cap
@@ -412,33 +490,39 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
   uint32_t fphase = 0;
   int it = 0;                                              // tiles so far: buffers and phases follow it
   int turn = 0;                                            // it % 3
-
-  for (;;) {
-    bool ok = lat_wait(&s->frag_full[fslot], fphase, abort_flag);
+  LatFragment f;
+  LatQueries<HG> queries;
+  bool ok;
+  auto next_fragment = [&](LatFragment& to) {
+    ok = lat_wait(&s->frag_full[fslot], fphase, abort_flag);
     if (group_any(bar_id, !ok)) return false;
-    const LatFragment f = s->frag[fslot];
+    to = s->frag[fslot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&s->frag_empty[fslot]);
     if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
-    if (!f.valid) return true;
-
+    if (to.valid) queries.load(a, to, group, tid);
+    return true;
+  };
+  if (!next_fragment(f)) return false;
+  while (f.valid) {
     // The earlier fragment's score MMAs are done (its last s_full was waited for): their operand
     // may be overwritten.
-    const float qscale = lat_load_queries<HG>(a, f, smem + SM::kOffQ, group, tid);
-    if ((tid & 15) == 0) s->inv[group][tid >> 4] = qscale * (a.sm_scale * (capped ? 1.0f : kLog2e));
+    const float qscale = queries.store(smem + SM::kOffQ, group, tid);
+    if (tid % (128 / C) == 0) s->inv[group][tid / (128 / C)] = qscale * (a.sm_scale * (capped ? 1.0f : kLog2e));
     fence_proxy_async_smem();
-    if (group_any(bar_id, false)) return false;
+    group_sync(bar_id);
     if (tid == 0) mbar_arrive(&s->q_full);
-    float fac[8], nref[8], sum[8];                         // nref: code exponent of the reference minus the reference
+    float fac[C], nref[C], sum[C];                         // nref: code exponent of the reference minus the reference
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < C; ++c) {
       fac[c] = s->inv[group][c];
       nref[c] = kLatNoRef;
       sum[c] = 0.0f;
     }
-    const int query = (f.col0 + group * 8) / a.Hq;
+    const float ref_exp = lat_ref_exponent(f.len);
+    const int query = (f.col0 + group * C) / a.Hq;
     const int sees_min = f.sees0 + query;                  // of this group's first column
-    const int next_query = (query + 1) * a.Hq - (f.col0 + group * 8);  // columns until the next query
+    const int next_query = (query + 1) * a.Hq - (f.col0 + group * C);  // columns until the next query
 
     for (int tile = f.tile0; tile < f.tile1; ++tile, ++it, turn = turn == 2 ? 0 : turn + 1) {
       const int buf = it & 1;
@@ -449,22 +533,24 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->tab_empty[ahead]);
       // the reference of a column bounds score + log2(page scale): the weights that meet the codes
-      const float bound = kLatPExp + kLatHeadroom - (sc > 0.0f ? __log2f(sc) : -100.0f);
-      float2 fs[4];
+      const float bound = kLatTopExp - (sc > 0.0f ? __log2f(sc) : -100.0f);
+      float2 fs[C / 2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fs[i] = make_float2(fac[2 * i] * sc, fac[2 * i + 1] * sc);
+      for (int i = 0; i < C / 2; ++i) fs[i] = make_float2(fac[2 * i] * sc, fac[2 * i + 1] * sc);
       ok = lat_wait(&s->s_full[buf], phase, abort_flag) && ok;
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      float t[8];
+      float t[C];
       {
-        float v[16];
-        tmem_load_16(lane_base + SM::kTmemS + buf * SM::kQRows + group * 16, v);
+        float v[2 * C];
+        const uint32_t at = lane_base + SM::kTmemS + buf * SM::kQRows + group * 2 * C;
+        if constexpr (C == 16) tmem_load_32(at, v);
+        else tmem_load_16(at, v);
         tc_fence_before();
         if (lane == 0) mbar_arrive(&s->s_empty[buf]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = __fmul2_rn(__ffma2_rn(make_float2(v[8 + 2 * i], v[9 + 2 * i]), make_float2(0.0625f, 0.0625f),
+        for (int i = 0; i < C / 2; ++i) {
+          const float2 x = __fmul2_rn(__ffma2_rn(make_float2(v[C + 2 * i], v[C + 1 + 2 * i]), make_float2(0.0625f, 0.0625f),
                                                  make_float2(v[2 * i], v[2 * i + 1])),
                                       fs[i]);
           t[2 * i] = x.x;
@@ -475,26 +561,26 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       if (isnan(t[0])) {
         bad = true;
 #pragma unroll
-        for (int c = 1; c < 8; ++c) bad = bad && isnan(t[c]);
+        for (int c = 1; c < C; ++c) bad = bad && isnan(t[c]);
       }
       if (capped) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) t[c] = cap2 - 2.0f * cap2 * __fdividef(1.0f, 1.0f + exp2_fast(t[c] * cap_in));
+        for (int c = 0; c < C; ++c) t[c] = cap2 - 2.0f * cap2 * __fdividef(1.0f, 1.0f + exp2_fast(t[c] * cap_in));
       }
       const int pos = tile * kLatTile + tid;
       if ((tile + 1) * kLatTile > min(sees_min, f.len)) {
         int sees = sees_min, left = next_query;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < C; ++c) {
           if (pos >= min(sees, f.len)) t[c] = -INFINITY;
           if (--left == 0) { left = a.Hq; ++sees; }
         }
       }
       // the weights' exponents, and whether one passes its bound (fmaxf passes over NaN; a column that
       // has no reference yet raises the flag with its first finite score)
-      float w[8], top = -INFINITY;
+      float w[C], top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < C; ++c) {
         w[c] = t[c] + nref[c];
         top = fmaxf(top, w[c]);
       }
@@ -502,12 +588,12 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       // were none.
       if (!ok) flag[turn] = 2;
       else if (top > bound) atomicOr(const_cast<int*>(&flag[turn]), 1);
-      uint32_t hi[2], lo[2], lo2[2];
+      uint32_t hi[C / 4], lo[C / 4], lo2[C / 4];
       for (bool again = false;; again = true) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = exp2_fast(w[c]);
+        for (int c = 0; c < C; ++c) w[c] = exp2_fast(w[c]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C / 4; ++i) {
           uint16_t h[2], l[2], l2[2];
           split_weights(w[4 * i] * sc, w[4 * i + 1] * sc, h[0], l[0], l2[0]);
           split_weights(w[4 * i + 2] * sc, w[4 * i + 3] * sc, h[1], l[1], l2[1]);
@@ -523,21 +609,21 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
         if (raised & 2) return false;
         if (!raised) break;
         // new references: the largest over the tile, where that is larger
-        const float lg = kLatPExp + kLatHeadroom - bound;
+        const float lg = kLatTopExp - bound;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < C; ++c) {
           const float x = isnan(t[c]) ? -INFINITY : t[c] + lg;
           const int m = __reduce_max_sync(0xffffffffu, float_order(x));
           if (lane == 0) s->red[group][warp][c] = order_float(m);
         }
         ok = tile == f.tile0 || lat_wait(&s->p_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort_flag);
         if (group_any(bar_id, !ok)) return false;
-        float alpha[8];
+        float alpha[C];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < C; ++c) {
           const float m = fmaxf(fmaxf(s->red[group][0][c], s->red[group][1][c]),
                                 fmaxf(s->red[group][2][c], s->red[group][3][c]));
-          const float next = fminf(nref[c], kLatPExp - m); // m = -inf: as it was
+          const float next = fminf(nref[c], ref_exp - m); // m = -inf: as it was
           alpha[c] = exp2_fast(next - nref[c]);
           nref[c] = next;
           sum[c] *= alpha[c];
@@ -547,11 +633,12 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
           tc_fence_after();
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
-            float x[24];
-            tmem_load_16_8(acc_hi + m * SM::kPRows, acc_lo2 + m * SM::kPRows, x);
+            float x[3 * C];
+            load_acc(m, x);
 #pragma unroll
-            for (int i = 0; i < 24; ++i) x[i] *= alpha[i & 7];
-            tmem_store_16_8(acc_hi + m * SM::kPRows, acc_lo2 + m * SM::kPRows, x);
+            for (int i = 0; i < 3 * C; ++i) x[i] *= alpha[i & (C - 1)];
+            if constexpr (C == 16) tmem_store_32_16(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
+            else tmem_store_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -561,8 +648,14 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       // the flag of the tile after the next: read before this barrier, raised after the next one
       if (tid == 0) flag[turn == 0 ? 2 : turn - 1] = 0;
       uint8_t* pb = smem + SM::kOffP + buf * SM::kPBytes + tid * 16;
-      *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-      *reinterpret_cast<uint2*>(pb + block2 * (16 * kLatTile) + half8) = make_uint2(lo2[0], lo2[1]);
+      if constexpr (C == 16) {
+        *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(pb + (block + 1) * (16 * kLatTile)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(pb + block2 * (16 * kLatTile)) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+      } else {
+        *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+        *reinterpret_cast<uint2*>(pb + block2 * (16 * kLatTile) + at2) = make_uint2(lo2[0], lo2[1]);
+      }
       if (bad) {
         // the row must not reach columns that give it no weight (0 x NaN): its values become 0, the
         // weights of the columns that do see it are NaN themselves
@@ -575,32 +668,36 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->p_full[buf]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] += w[c];
+      for (int c = 0; c < C; ++c) sum[c] += w[c];
     }
 
-    // ---- the fragment's result: the columns' sums over all threads, then the accumulators
+    // ---- the fragment's result: the columns' sums over all threads, then the accumulators; the next
+    // fragment's queries are on their way meanwhile
+    LatFragment next;
+    if (!next_fragment(next)) return false;
     ok = lat_wait(&s->p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag);
-    // lane bits 4 .. 2 choose a half of the columns each: four lanes end with parts of one column's sum
+    // each of the upper lane bits chooses a half of the columns: 32 / C lanes end with parts of one column's sum
+    constexpr int kShare = 32 / C;
 #pragma unroll
-    for (int h = 4; h; h >>= 1) {
-      const bool upper = (lane & (4 * h)) != 0;
+    for (int h = C / 2; h; h >>= 1) {
+      const bool upper = (lane & (kShare * h)) != 0;
 #pragma unroll
       for (int c = 0; c < h; ++c) {
         const float keep = upper ? sum[c + h] : sum[c], give = upper ? sum[c] : sum[c + h];
-        sum[c] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * h);
+        sum[c] = keep + __shfl_xor_sync(0xffffffffu, give, kShare * h);
       }
     }
-    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
-    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-    if ((lane & 3) == 0) s->red[group][warp][lane >> 2] = sum[0];
+#pragma unroll
+    for (int d = kShare / 2; d; d >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
+    if (lane % kShare == 0) s->red[group][warp][lane / kShare] = sum[0];
     if (group_any(bar_id, !ok)) return false;
     tc_fence_after();
-    const int live = min(8, f.cols - group * 8);
-    const size_t row0 = static_cast<size_t>(f.row0) + group * 8;
-    const size_t part0 = static_cast<size_t>(max(f.slot, 0)) * HG + group * 8;
-    if (tid < 8) {
+    const int live = min(C, f.cols - group * C);
+    const size_t row0 = static_cast<size_t>(f.row0) + group * C;
+    const size_t part0 = static_cast<size_t>(max(f.slot, 0)) * HG + group * C;
+    if (tid < C) {
       const float l = (s->red[group][0][tid] + s->red[group][1][tid]) + (s->red[group][2][tid] + s->red[group][3][tid]);
-      const float m = pick8(nref, tid);                    // l sums 2^(score + m)
+      const float m = pick(nref, tid);                     // l sums 2^(score + m)
       if (tid < live) {
         if (f.slot >= 0) a.part_ml[part0 + tid] = make_float2(m, l);
         else if (a.lse) a.lse[row0 + tid] = l == 0.0f ? -INFINITY : (log2f(l) - m) * kLn2;
@@ -610,15 +707,15 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     }
     group_sync(bar_id);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) sum[c] = s->inv[group][c];
+    for (int c = 0; c < C; ++c) sum[c] = s->inv[group][c];
 #pragma unroll 1
     for (int m = 0; m < 4; ++m) {
-      float x[24];
-      tmem_load_16_8(acc_hi + m * SM::kPRows, acc_lo2 + m * SM::kPRows, x);
+      float x[3 * C];
+      load_acc(m, x);
       const int d = m * 128 + tid;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float y = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]);
+      for (int c = 0; c < C; ++c) {
+        const float y = fmaf(fmaf(x[2 * C + c], 0.03125f, x[C + c]), 0.03125f, x[c]);
         if (c < live) {
           if (f.slot < 0) a.o[(row0 + c) * kLatDv + d] = __float2bfloat16(sum[c] == 0.0f ? 0.0f : y * sum[c]);
           else a.part_o[(part0 + c) * kLatDv + d] = y;
@@ -627,7 +724,9 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     }
     tc_fence_before();
     group_sync(bar_id);                                    // red, inv and TMEM are read before what comes next
+    f = next;
   }
+  return true;
 }
 
 // ---------------------------------------------------------------- MMA warp
@@ -787,54 +886,56 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
   }
 }
 
-// Warp 0, one thread: the loads, a half of a tile at a time as P V frees them.
+// Warp 0: the loads, a half of a tile at a time as P V frees them. As in the MMA warp all lanes run
+// the loop and one issues: 43 cycles per copy, 100 to 150 from a divergent branch.
 template <int HG>
 __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtensorMap* tm_lat, const CUtensorMap* tm_rot,
-                                              typename LatSmem<HG>::Info* s, uint8_t* smem) {
+                                              typename LatSmem<HG>::Info* s, uint8_t* smem_any) {
   using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
+  const int lane = threadIdx.x & 31;
+  const bool leader = elect_one();
+  uint8_t* smem = smem_any;
   const int run = a.run, step = run ? run : 4, pieces = kLatTile / step;
   for (int it = 0;; ++it) {
     const int ahead = it % kLatAhead;
-    if (!lat_wait(&s->tab_full[ahead], (it / kLatAhead) & 1, abort_flag)) return false;
-    const int live = s->live[ahead];
+    if (!__all_sync(0xffffffffu, lat_wait(&s->tab_full[ahead], (it / kLatAhead) & 1, abort_flag))) return false;
+    const int live = __shfl_sync(0xffffffffu, s->live[ahead], 0);
     if (live < 0) return true;
-    int4 first[2] = {s->rows[ahead][0], s->rows[ahead][1]};            // pages of 64 and more need no others
+    const int4 mine = s->rows[ahead][lane];
     uint8_t* rot = smem + SM::kOffRot + it % SM::kRots * kLatRot;
-#pragma unroll
+#pragma unroll 1
     for (int half = 0; half < 2; ++half) {                 // rotary entries and chunks 0, 1; chunks 2, 3
       const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
       uint64_t* full = &s->kv_full[h.slot];
       uint8_t* dst = smem + h.slot * kLatHalf;
-      if (!lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag)) return false;
-      mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
-      if (run >= 64) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i < pieces && first[i].x >= 0) {
-            if (half == 0) tma_load_2d(rot + i * 64 * 64, tm_rot, full, 512, first[i].x);
-            tma_load_2d(dst + i * 64 * 128, tm_lat, full, half * 256, first[i].x);
-            tma_load_2d(dst + kLatChunk + i * 64 * 128, tm_lat, full, half * 256 + 128, first[i].x);
+      if (!__all_sync(0xffffffffu, lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag))) return false;
+      if (leader) mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
+      if (run) {
+#pragma unroll 1
+        for (int i = 0, at = 0; i < pieces; ++i, at += step) {
+          const int row = __shfl_sync(0xffffffffu, mine.x, i);
+          if (row >= 0 && leader) {
+            if (half == 0) tma_load_2d(rot + at * 64, tm_rot, full, 512, row);
+            tma_load_2d(dst + at * 128, tm_lat, full, half * 256, row);
+            tma_load_2d(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, row);
           }
         }
       } else {
 #pragma unroll 1
         for (int i = 0, at = 0; i < pieces; ++i, at += step) {
-          const int4 rows = s->rows[ahead][i];
-          if (rows.x < 0) continue;
-          if (run) {
-            if (half == 0) tma_load_2d(rot + at * 64, tm_rot, full, 512, rows.x);
-            tma_load_2d(dst + at * 128, tm_lat, full, half * 256, rows.x);
-            tma_load_2d(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, rows.x);
-          } else {
+          const int4 rows = make_int4(__shfl_sync(0xffffffffu, mine.x, i), __shfl_sync(0xffffffffu, mine.y, i),
+                                      __shfl_sync(0xffffffffu, mine.z, i), __shfl_sync(0xffffffffu, mine.w, i));
+          if (rows.x >= 0 && leader) {
             if (half == 0) tma_gather4(rot + at * 64, tm_rot, full, 512, rows);
             tma_gather4(dst + at * 128, tm_lat, full, half * 256, rows);
             tma_gather4(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, rows);
           }
         }
       }
+      __syncwarp();
     }
-    mbar_arrive(&s->tab_empty[ahead]);
+    if (leader) mbar_arrive(&s->tab_empty[ahead]);
   }
 }
 
@@ -906,8 +1007,10 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   const int gang_id = blockIdx.x >> a.gang_log, rank = blockIdx.x - (gang_id << a.gang_log);
   const int ngangs = static_cast<int>(min(static_cast<long long>(gridDim.x >> a.gang_log), total));
   const bool works = gang_id < ngangs;
+  long long p0 = 0, p1 = 0;
   if (works) {
-    const long long p0 = div_small(total * gang_id, ngangs);
+    p0 = div_small(total * gang_id, ngangs);
+    if (warp == 2) p1 = div_small(total * (gang_id + 1), ngangs);
     if (p0 >= before && p0 < before + mine) {
       long long off = before;
       for (int b = b0; b < b1; ++b) {
@@ -932,15 +1035,14 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   } else if (warp >= 4) {
     ok = lat_softmax_role<HG>(a, s, smem, tmem);
   } else if (warp == 2) {
-    if (lane == 0) ok = lat_schedule<HG>(a, s, total, ngangs, gang_id, rank);
+    if (lane == 0) ok = lat_schedule<HG>(a, s, total, ngangs, gang_id, rank, p0, p1);
     __syncwarp();
   } else if (warp == 1) {
     ok = lat_mma_role<HG>(s, smem, tmem);
   } else if (warp == 3) {
     ok = lat_table_role<HG>(a, s);
   } else {
-    if (lane == 0) ok = lat_load_role<HG>(a, &tm_lat, &tm_rot, s, smem);
-    __syncwarp();
+    ok = lat_load_role<HG>(a, &tm_lat, &tm_rot, s, smem);
     if (!ok) {
       // copies already in flight must land before the CTA's shared memory goes away
       const unsigned long long t0 = global_timer_ns();
@@ -968,25 +1070,27 @@ __global__ void __launch_bounds__(128) mla_fp8_join_kernel(const LatAttnArgs a) 
   const int cta = blockIdx.x, c = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int4 job = a.merge[cta];
   if (job.z == 0 || c >= job.y) return;
-  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? job.w : 2 * (cta + (i << a.gang_log))) * HG + c; };
-  float m = INFINITY;                                      // the part with the largest reference
-  for (int i = 0; i < job.z; ++i) m = fminf(m, a.part_ml[slot(i)].x);
-  float l = 0.0f, acc[16];
+  float m = kLatNoRef, l = 0.0f;                           // reference (the largest is the least m) and sum so far
+  float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+#pragma unroll 2
   for (int i = 0; i < job.z; ++i) {
-    const size_t at = slot(i);
+    const size_t at = static_cast<size_t>(i == 0 ? job.w : 2 * (cta + (i << a.gang_log))) * HG + c;
     const float2 ml = a.part_ml[at];
+    float4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[j * 32 + lane];
     if (ml.y == 0.0f) continue;
-    const float w = exp2f(m - ml.x);
-    l += w * ml.y;
+    const float next = fminf(m, ml.x), w0 = exp2f(next - m), w1 = exp2f(next - ml.x);
+    m = next;
+    l = l * w0 + ml.y * w1;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float4 x = reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[j * 32 + lane];
-      acc[4 * j] += w * x.x;
-      acc[4 * j + 1] += w * x.y;
-      acc[4 * j + 2] += w * x.z;
-      acc[4 * j + 3] += w * x.w;
+      acc[4 * j] = acc[4 * j] * w0 + x[j].x * w1;
+      acc[4 * j + 1] = acc[4 * j + 1] * w0 + x[j].y * w1;
+      acc[4 * j + 2] = acc[4 * j + 2] * w0 + x[j].z * w1;
+      acc[4 * j + 3] = acc[4 * j + 3] * w0 + x[j].w * w1;
     }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
