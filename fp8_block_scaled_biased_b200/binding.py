@@ -685,45 +685,70 @@ def mla_decode_fwd(q, kv_buffer, o, kv_indptr, kv_indices, kv_last_page_lens, sm
 
 
 # ---------------------------------------------------------------- 8-bit latent KV cache
+# These calls take a few microseconds on the GPU at decode sizes, so their checks are kept to one
+# test per tensor; _refuse says what is wrong once one has failed.
+def _refuse(t, dtype, name, dev, shape):
+    _cuda(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: all tensors must be on one device, got cuda:{t.get_device()} and cuda:{dev}")
+    raise ValueError(f"{name} must be a contiguous {shape} tensor, got {list(t.shape)} with strides {list(t.stride())}")
+
+
 def _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens):
-    """Checks the cache and page table that the 8-bit cache calls share; returns (batch, pages,
-    page_size, the table's length)."""
-    _cuda(kv_cache, FP8, "kv_cache")
-    _cuda(kv_scale, torch.float32, "kv_scale")
-    if kv_cache.dim() != 4 or kv_cache.shape[2] != 1 or kv_cache.shape[3] != MLA_QK_HEAD_DIM \
+    """Checks the cache and page table that the 8-bit cache calls share; returns (device index,
+    batch, pages, page_size, the table's length)."""
+    dev = kv_cache.get_device()
+    shape = kv_cache.shape
+    if kv_cache.dtype is not FP8 or dev < 0 or len(shape) != 4 or shape[2] != 1 or shape[3] != MLA_QK_HEAD_DIM \
             or not kv_cache.is_contiguous():
-        raise ValueError(f"kv_cache must be a contiguous [pages, page_size, 1, {MLA_QK_HEAD_DIM}] tensor")
-    pages, page_size = kv_cache.shape[0], kv_cache.shape[1]
-    if kv_scale.shape != (pages, 1) or not kv_scale.is_contiguous():
-        raise ValueError(f"kv_scale must be a contiguous [{pages}, 1] tensor")
-    batch = kv_last_page_lens.numel()
-    for t, name in ((kv_indptr, "kv_indptr"), (kv_indices, "kv_indices"), (kv_last_page_lens, "kv_last_page_lens")):
-        _cuda(t, torch.int32, name)
-        if t.dim() != 1 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 1-D tensor")
-    if kv_indptr.numel() != batch + 1:
-        raise ValueError("kv_indptr must hold one entry more than kv_last_page_lens")
-    return batch, pages, page_size, kv_indices.numel()
+        _refuse(kv_cache, FP8, "kv_cache", dev, f"[pages, page_size, 1, {MLA_QK_HEAD_DIM}]")
+    pages = shape[0]
+    if kv_scale.dtype is not torch.float32 or kv_scale.get_device() != dev or kv_scale.shape != (pages, 1) \
+            or not kv_scale.is_contiguous():
+        _refuse(kv_scale, torch.float32, "kv_scale", dev, f"[{pages}, 1]")
+    if kv_last_page_lens.dtype is not torch.int32 or kv_last_page_lens.get_device() != dev \
+            or kv_last_page_lens.dim() != 1 or not kv_last_page_lens.is_contiguous():
+        _refuse(kv_last_page_lens, torch.int32, "kv_last_page_lens", dev, "[batch]")
+    batch = kv_last_page_lens.shape[0]
+    _ranges(kv_indptr, "kv_indptr", dev, batch)
+    if kv_indices.dtype is not torch.int32 or kv_indices.get_device() != dev or kv_indices.dim() != 1 \
+            or not kv_indices.is_contiguous():
+        _refuse(kv_indices, torch.int32, "kv_indices", dev, "[entries]")
+    return dev, batch, pages, shape[1], kv_indices.shape[0]
 
 
-def _ranges(indptr, name, batch):
-    _cuda(indptr, torch.int32, name)
-    if indptr.shape != (batch + 1,) or not indptr.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of {batch + 1} entries")
+def _ranges(indptr, name, dev, batch):
+    if indptr.dtype is not torch.int32 or indptr.get_device() != dev or indptr.shape != (batch + 1,) \
+            or not indptr.is_contiguous():
+        _refuse(indptr, torch.int32, name, dev, f"[{batch + 1}]")
 
 
-def _call_on(device, name, tensors, *args):
-    """Calls the library on `device`'s current stream; every tensor must lie on that device."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: all tensors must be on one device, got {device} and {t.device}")
-    lib = load_library()
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            rc = getattr(lib, name)(*args, _stream())
+def _latent_rows(t, name, dev):
+    """Checks bf16 rows [T, 576] of unit column stride; returns (T, row stride)."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _refuse(t, torch.bfloat16, name, dev, f"[T, {MLA_QK_HEAD_DIM}]")
+    if t.dim() != 2 or t.shape[1] != MLA_QK_HEAD_DIM:
+        raise ValueError(f"{name} must be [T, {MLA_QK_HEAD_DIM}]")
+    if t.is_contiguous():               # (which a single row is, whatever its stride says)
+        return t.shape[0], MLA_QK_HEAD_DIM
+    return t.shape[0], _row_major(t, name)
+
+
+def _raw_stream(dev):
+    # torch.cuda.current_stream(dev) builds a Stream object, which takes 3 us
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _call_on(dev, name, *args):
+    """Calls the library on the current stream of device `dev`."""
+    fn = getattr(load_library(), name)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
     else:
-        rc = getattr(lib, name)(*args, _stream())
-    _check(name, rc)
+        rc = fn(*args, _raw_stream(dev))
+    if rc:
+        _check(name, rc)
 
 
 def mla_kv_append_fp8(kv_new, append_indptr, kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens):
@@ -731,35 +756,23 @@ def mla_kv_append_fp8(kv_new, append_indptr, kv_cache, kv_scale, kv_indptr, kv_i
     tokens of sequence b, whose page table counts them in) to the 8-bit latent cache: kv_cache
     fp8 [pages, page_size, 1, 576] and kv_scale fp32 [pages, 1], both updated in place. A page
     whose scale grows has its earlier rows re-coded."""
-    batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
-    _cuda(kv_new, torch.bfloat16, "kv_new")
-    ld = _row_major(kv_new, "kv_new")
-    if kv_new.shape[1] != MLA_QK_HEAD_DIM:
-        raise ValueError(f"kv_new must be [T, {MLA_QK_HEAD_DIM}]")
-    T = kv_new.shape[0]
-    if T <= 1:
-        ld = MLA_QK_HEAD_DIM            # the stride of a single row says nothing
-    _ranges(append_indptr, "append_indptr", batch)
-    _call_on(kv_cache.device, "mla_kv_append_fp8",
-             (kv_new, append_indptr, kv_scale, kv_indptr, kv_indices, kv_last_page_lens),
-             _ptr(kv_new), ld, _ptr(append_indptr), _ptr(kv_cache), _ptr(kv_scale), _ptr(kv_indptr), _ptr(kv_indices),
-             _ptr(kv_last_page_lens), batch, T, pages, page_size, n_idx)
+    dev, batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
+    T, ld = _latent_rows(kv_new, "kv_new", dev)
+    _ranges(append_indptr, "append_indptr", dev, batch)
+    _call_on(dev, "mla_kv_append_fp8", kv_new.data_ptr(), ld, append_indptr.data_ptr(), kv_cache.data_ptr(),
+             kv_scale.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_last_page_lens.data_ptr(), batch, T,
+             pages, page_size, n_idx)
 
 
 def mla_kv_gather_fp8(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens, out_indptr, out):
     """Reads tokens back from the 8-bit latent cache: out bf16 [T, 576] rows out_indptr[b] ..
     out_indptr[b+1] become the first tokens of sequence b. Returns out."""
-    batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
-    _cuda(out, torch.bfloat16, "out")
-    ld = _row_major(out, "out")
-    if out.shape[1] != MLA_QK_HEAD_DIM:
-        raise ValueError(f"out must be [T, {MLA_QK_HEAD_DIM}]")
-    if out.shape[0] <= 1:
-        ld = MLA_QK_HEAD_DIM
-    _ranges(out_indptr, "out_indptr", batch)
-    _call_on(kv_cache.device, "mla_kv_gather_fp8", (kv_scale, kv_indptr, kv_indices, kv_last_page_lens, out_indptr, out),
-             _ptr(kv_cache), _ptr(kv_scale), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_lens),
-             _ptr(out_indptr), _ptr(out), ld, batch, out.shape[0], pages, page_size, n_idx)
+    dev, batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
+    T, ld = _latent_rows(out, "out", dev)
+    _ranges(out_indptr, "out_indptr", dev, batch)
+    _call_on(dev, "mla_kv_gather_fp8", kv_cache.data_ptr(), kv_scale.data_ptr(), kv_indptr.data_ptr(),
+             kv_indices.data_ptr(), kv_last_page_lens.data_ptr(), out_indptr.data_ptr(), out.data_ptr(), ld, batch, T,
+             pages, page_size, n_idx)
     return out
 
 
@@ -770,41 +783,39 @@ def mla_fp8_workspace_bytes(num_heads, num_q):
 
 def _mla_fp8_attention(name, q, qo_indptr, kv_cache, kv_scale, o, kv_indptr, kv_indices, kv_last_page_lens, sm_scale,
                        logit_cap, lse, workspace):
-    batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
-    _cuda(q, torch.bfloat16, "q")
-    _cuda(o, torch.bfloat16, "o")
-    if q.dim() != 3 or q.shape[2] != MLA_QK_HEAD_DIM or not q.is_contiguous():
-        raise ValueError(f"q must be a contiguous [rows, heads, {MLA_QK_HEAD_DIM}] tensor")
+    dev, batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
+    if q.dtype is not torch.bfloat16 or q.get_device() != dev or q.dim() != 3 or q.shape[2] != MLA_QK_HEAD_DIM \
+            or not q.is_contiguous():
+        _refuse(q, torch.bfloat16, "q", dev, f"[rows, heads, {MLA_QK_HEAD_DIM}]")
     rows, heads = q.shape[0], q.shape[1]
-    if o.shape != (rows, heads, MLA_V_HEAD_DIM) or not o.is_contiguous():
-        raise ValueError(f"o must be a contiguous [{rows}, {heads}, {MLA_V_HEAD_DIM}] tensor")
-    if lse is not None:
-        _cuda(lse, torch.float32, "lse")
-        if lse.shape != (rows, heads) or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous [{rows}, {heads}] tensor")
+    if o.dtype is not torch.bfloat16 or o.get_device() != dev or o.shape != (rows, heads, MLA_V_HEAD_DIM) \
+            or not o.is_contiguous():
+        _refuse(o, torch.bfloat16, "o", dev, f"[{rows}, {heads}, {MLA_V_HEAD_DIM}]")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (rows, heads)
+                            or not lse.is_contiguous()):
+        _refuse(lse, torch.float32, "lse", dev, f"[{rows}, {heads}]")
     if qo_indptr is None:
         if rows != batch:
             raise ValueError(f"q must hold one row per sequence ({batch}), got {rows}")
         ranges, sizes = (), (batch, heads)
     else:
-        _ranges(qo_indptr, "qo_indptr", batch)
-        ranges, sizes = (_ptr(qo_indptr),), (batch, rows, heads)
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(MLA_QK_HEAD_DIM)
+        _ranges(qo_indptr, "qo_indptr", dev, batch)
+        ranges, sizes = (qo_indptr.data_ptr(),), (batch, rows, heads)
     if workspace is None:
         need = mla_fp8_workspace_bytes(heads, rows)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
-        _cuda(workspace, torch.uint8, "workspace")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    _call_on(kv_cache.device, name,
-             (q, qo_indptr, kv_scale, o, kv_indptr, kv_indices, kv_last_page_lens, lse, workspace),
-             _ptr(q), *ranges, _ptr(kv_cache), _ptr(kv_scale), _ptr(o), _ptr(kv_indptr), _ptr(kv_indices),
-             _ptr(kv_last_page_lens), _ptr(lse), *sizes, pages, page_size, n_idx, float(sm_scale), float(logit_cap),
-             _ptr(workspace), 0 if workspace is None else workspace.numel())
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(workspace, torch.uint8, "workspace", dev, "byte")
+    _call_on(dev, name, q.data_ptr(), *ranges, kv_cache.data_ptr(), kv_scale.data_ptr(), o.data_ptr(),
+             kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_last_page_lens.data_ptr(),
+             None if lse is None else lse.data_ptr(), *sizes, pages, page_size, n_idx,
+             _MLA_SCALE if sm_scale is None else float(sm_scale), float(logit_cap),
+             None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return o
+
+
+_MLA_SCALE = 1.0 / math.sqrt(MLA_QK_HEAD_DIM)
 
 
 def mla_decode_fp8_fwd(q, kv_cache, kv_scale, o, kv_indptr, kv_indices, kv_last_page_lens, sm_scale=None,

@@ -114,9 +114,11 @@ int device_setup(int* sm_count) {
     if (r == cudaSuccess)
       r = cudaFuncSetAttribute(mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMlaSmemBytes);
     if (r == cudaSuccess)
-      r = cudaFuncSetAttribute(mla_fp8_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<16>::kBytes);
+      r = cudaFuncSetAttribute(mla_fp8_kernel<16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<16>::kBytes);
     if (r == cudaSuccess)
-      r = cudaFuncSetAttribute(mla_fp8_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<32>::kBytes);
+      r = cudaFuncSetAttribute(mla_fp8_kernel<16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<16>::kBytes);
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(mla_fp8_kernel<32, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<32>::kBytes);
     if (r == cudaSuccess)
       r = cudaFuncSetAttribute(sort_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(sort_scatter_smem(kSortMaxExperts)));
@@ -1232,14 +1234,14 @@ size_t mla_fp8_workspace(int num_heads, int num_q) {
 
 }  // extern "C"
 
-template <int HG>
+template <int HG, bool SMALL>
 static int lat_launch(const char* name, LatAttnArgs a, const CUtensorMap& lat, const CUtensorMap& rot, int ctas,
                       void* workspace, cudaStream_t st) {
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.merge = reinterpret_cast<int4*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + lat_parts_offset());
   a.part_o = reinterpret_cast<float*>(ws + lat_acc_offset(HG));
-  mla_fp8_kernel<HG><<<ctas, LatSmem<HG>::kThreads, LatSmem<HG>::kBytes, st>>>(lat, rot, a);
+  mla_fp8_kernel<HG, SMALL><<<ctas, kLatThreads<HG, SMALL>, LatSmem<HG>::kBytes, st>>>(lat, rot, a);
   if (int rc = check_launch(name)) return rc;
   // launched while the attention kernel runs (programmatic dependence): it waits for its end itself
   cudaLaunchConfig_t cfg{};
@@ -1294,29 +1296,33 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
   a.Hq = num_heads;
   a.sm_scale = sm_scale;
   a.logit_cap = logit_cap;
-  // rows that a page holds together come by one TMA box: the largest power of two in page_size
-  a.run = page_size % 8 ? 0 : std::min(kLatTile, page_size & -page_size);
+  a.cache = kv_cache;
+  // Rows that a page holds together come by TMA boxes: the largest power of two in page_size. Below 32
+  // rows the boxes take longer to issue (80 cycles each, five per box of rows) than HBM needs for the
+  // tile (3250), and four warps copy the rows instead; with 16 columns, whose threads leave room for them.
+  a.run = std::min(kLatTile, page_size & -page_size);
+  const bool small = a.run < 32;
   CUtensorMap lat, rot;
   std::memset(&lat, 0, sizeof(lat));
   std::memset(&rot, 0, sizeof(rot));
-  if (num_indices > 0) {
+  if (num_indices > 0 && !small) {
     const uint64_t rows = static_cast<uint64_t>(num_pages) * page_size;
-    const uint32_t box = a.run ? a.run : 1;
-    if (int rc = make_map_2d(&lat, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kv_cache, rows, kLatDk, kLatDk, 128, box,
+    if (int rc = make_map_2d(&lat, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kv_cache, rows, kLatDk, kLatDk, 128, a.run,
                              CU_TENSOR_MAP_SWIZZLE_128B))
       return rc;
-    if (int rc = make_map_2d(&rot, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kv_cache, rows, kLatDk, kLatDk, 64, box,
+    if (int rc = make_map_2d(&rot, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kv_cache, rows, kLatDk, kLatDk, 64, a.run,
                              CU_TENSOR_MAP_SWIZZLE_64B))
       return rc;
   }
   // 16 columns per CTA where a sequence has no more, else 32; a gang of CTAs for its column groups
   const long long cols = (static_cast<long long>(num_q) * num_heads + batch - 1) / batch;
-  const int hg = cols <= 16 ? 16 : 32;
+  const int hg = cols <= 16 || small ? 16 : 32;
   a.gang_log = cols > 3 * hg ? 2 : cols > hg ? 1 : 0;
   const int ctas = std::max(1, std::min(sms, kLatMaxCtas) >> a.gang_log) << a.gang_log;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return hg == 16 ? lat_launch<16>(name, a, lat, rot, ctas, workspace, st)
-                  : lat_launch<32>(name, a, lat, rot, ctas, workspace, st);
+  if (small) return lat_launch<16, true>(name, a, lat, rot, ctas, workspace, st);
+  return hg == 16 ? lat_launch<16, false>(name, a, lat, rot, ctas, workspace, st)
+                  : lat_launch<32, false>(name, a, lat, rot, ctas, workspace, st);
 }
 
 int mla_decode_fp8_fwd(const uint16_t* q, const uint8_t* kv_cache, const float* kv_scale, uint16_t* o,

@@ -18,14 +18,14 @@
 // Products of codes are exact and the MMA sums in fp32. Scales of pages (one per token row,
 // i.e. per TMEM lane) multiply the scores, and the weights before they are split.
 //
-// A CTA holds `HG` columns and walks 128-token tiles through two shared-memory stages:
+// A CTA holds `HG` columns and walks 128-token tiles through a ring of half tiles in shared memory:
 //   warp 3      page table: the tiles' rows and scales, some tiles ahead
-//   warp 0      TMA: boxes of 8 to 128 rows that a page holds together; gather4 for other page
-//               sizes. A stage is loaded and freed in two halves
+//   warp 0      TMA: boxes of 32 to 128 rows that a page holds together, half a tile at a time
+//   warps 12-15 for smaller pages instead: 16-byte asynchronous copies
 //   warp 1      the MMAs: scores of the next tile are issued ahead of this tile's P V if its
 //               rows have landed, else after
 //   warp 2      the work list (below), TMEM
-//   warps 4-11  two warpgroups, half of the columns each, a token per thread: online softmax. The running
+//   warps 4..   one warpgroup per 8 columns, a token per thread: online softmax. The running
 //               reference of a column only moves when a score passes it by more than one
 //               (base 2), and then the accumulators in TMEM are rescaled.
 //
@@ -60,6 +60,7 @@ constexpr float kLatNoRef = 1e30f;                         // reference of a col
 struct LatAttnArgs {
   const __nv_bfloat16* q;        // [num_q, Hq, 576]
   const int32_t* qo_indptr;      // [B + 1], or null: one query token per sequence
+  const uint8_t* cache;          // [num_pages * page_size, 576]
   const float* scale;
   PageTable table;
   __nv_bfloat16* o;              // [num_q, Hq, 512]
@@ -68,7 +69,7 @@ struct LatAttnArgs {
   float2* part_ml;               // [2 * CTAs, HG]: reference and sum
   int4* merge;                   // [CTAs]: first row, columns, parts, first part's slot (parts 0: nothing)
   int num_q, Hq, gang_log;       // CTAs of a gang: 1, 2 or 4
-  int run;                       // rows per TMA box (8 .. 128), or 0: gather4
+  int run;                       // rows per TMA box: 32, 64 or 128
   float sm_scale, logit_cap;
 };
 
@@ -104,21 +105,20 @@ struct LatSmem {
   // TMEM columns: two score buffers, four accumulators of 128 value columns
   static constexpr int kTmemS = 0, kTmemO = 2 * kQRows;
   static constexpr int kTmemCols = (kTmemO + 4 * kPRows <= 256) ? 256 : 512;
-  static constexpr int kGroups = HG / 8, kCols = 8;   // softmax warpgroups, columns of each
-  static constexpr int kThreads = 128 + 128 * kGroups;
+  static constexpr int kGroups = HG / 8;                   // softmax warpgroups, 8 columns each
   struct Info {
     LatFragment frag[2];
-    // per tile: first rows of the runs (or four rows per group), -1 for none; tokens' scales
-    int4 rows[kLatAhead][32];
+    // per tile: the tokens' rows (or only those that begin a box), -1 for none; the tokens' scales
+    int rows[kLatAhead][kLatTile];
     float scale[kLatAhead][kLatTile];
     int live[kLatAhead];          // rows to be loaded; -1: the end of the list
-    uint64_t tab_full[kLatAhead], tab_empty[kLatAhead];
-    float red[kGroups][4][kCols], inv[kGroups][kCols];
+    uint64_t rows_full[kLatAhead], scale_full[kLatAhead], tab_empty[kLatAhead];
+    float red[kGroups][4][8], inv[kGroups][8], qfac[2][kGroups][8];
     uint64_t kv_full[kHalves], kv_empty[kHalves];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t frag_full[2], frag_empty[2], q_full;
     int flag[kGroups][3];         // a score passed its reference's bound (1), a wait failed (2); tiles take turns
-    long long scan[kThreads / 32];
+    long long scan[24];
     long long start_off;          // position of the first sequence of this CTA's share,
     int start_b;                  // the sequence, and its shape
     LatShape start;
@@ -127,6 +127,9 @@ struct LatSmem {
   };
   static constexpr int kBytes = kOffInfo + static_cast<int>(sizeof(Info)) + 1024;   // + alignment
 };
+
+template <int HG, bool SMALL>
+constexpr int kLatThreads = 128 + 128 * LatSmem<HG>::kGroups + (SMALL ? 128 : 0);
 
 // Position of a half of a tile in the ring: its slot, and the parity of the slot's use.
 struct LatHalf {
@@ -139,13 +142,8 @@ __device__ __forceinline__ LatHalf lat_half(int n) {
 }
 
 // ---------------------------------------------------------------- PTX
-__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int4 rows) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z),
-      "r"(rows.w)
-      : "memory");
+__device__ __forceinline__ void cp_async_16(uint32_t smem_dst, const void* gmem_src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gmem_src) : "memory");
 }
 // 32 lanes x consecutive fp32 columns (in one or two runs): loads are waited for once, stores are not.
 __device__ __forceinline__ void tmem_load_16(uint32_t at0, float (&v)[16]) {
@@ -154,18 +152,6 @@ __device__ __forceinline__ void tmem_load_16(uint32_t at0, float (&v)[16]) {
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-      : "r"(at0)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_load_32(uint32_t at0, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(at0)
       : "memory");
 }
@@ -180,22 +166,6 @@ __device__ __forceinline__ void tmem_load_16_8(uint32_t at0, uint32_t at1, float
       : "r"(at0), "r"(at1)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load_32_16(uint32_t at0, uint32_t at1, float (&v)[48]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%48];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47},"
-      " [%49];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
-        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
-        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47])
-      : "r"(at0), "r"(at1)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_store_16_8(uint32_t at0, uint32_t at1, const float (&v)[24]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%24], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n\t"
@@ -203,20 +173,6 @@ __device__ __forceinline__ void tmem_store_16_8(uint32_t at0, uint32_t at1, cons
       ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
         "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
         "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "r"(at0), "r"(at1)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_store_32_16(uint32_t at0, uint32_t at1, const float (&v)[48]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%48], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\t"
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%49], {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,"
-      "%46,%47};"
-      ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
-        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
-        "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]),
-        "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "f"(v[32]), "f"(v[33]), "f"(v[34]), "f"(v[35]),
-        "f"(v[36]), "f"(v[37]), "f"(v[38]), "f"(v[39]), "f"(v[40]), "f"(v[41]), "f"(v[42]), "f"(v[43]), "f"(v[44]),
-        "f"(v[45]), "f"(v[46]), "f"(v[47]), "r"(at0), "r"(at1)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -305,9 +261,11 @@ __device__ __noinline__ LatShape lat_shape(const LatAttnArgs& a, int b, int HG) 
   return s;
 }
 
+__device__ __noinline__ long long lat_div_large(long long a, long long b) { return a / b; }
 // Quotient of non-negative 64-bit numbers that mostly fit 32 bits.
-__device__ __noinline__ long long div_small(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+__device__ __forceinline__ long long lat_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return lat_div_large(a, b);
 }
 
 // Warp 2, one lane: the fragments of positions [p0, p1) of the work list, through the ring.
@@ -331,7 +289,7 @@ __device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatS
       off += static_cast<long long>(sh.groups) * sh.tiles;
       sh = lat_shape(a, ++b, HG);
     }
-    const int v = static_cast<int>(div_small(p - off, sh.tiles));
+    const int v = sh.groups == 1 ? 0 : static_cast<int>(lat_div(p - off, sh.tiles));
     const long long base = off + static_cast<long long>(v) * sh.tiles;
     const int t0 = static_cast<int>(p - base);
     const int t1 = static_cast<int>(min(static_cast<long long>(sh.tiles), p1 - base));
@@ -342,12 +300,12 @@ __device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatS
     if (u >= sh.units) continue;
     LatFragment f{};
     f.first = sh.first;
-    const int c0 = u * HG, query = c0 / a.Hq;
+    const int c0 = u * HG, query = sh.n == 1 ? 0 : c0 / a.Hq;
     f.col0 = c0 - query * a.Hq;
     f.cols = min(HG, sh.n * a.Hq - c0);
     f.row0 = sh.qlo * a.Hq + c0;
     f.sees0 = sh.len - sh.n + query + 1;
-    f.len = max(0, min(sh.len, f.sees0 + (f.col0 + f.cols - 1) / a.Hq));
+    f.len = max(0, min(sh.len, f.sees0 + (sh.n == 1 ? 0 : (f.col0 + f.cols - 1) / a.Hq)));
     const int tiles = max(1, (f.len + kLatTile - 1) / kLatTile);
     f.tile0 = t0;
     f.tile1 = min(t1, tiles);
@@ -358,7 +316,7 @@ __device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatS
       f.slot = 2 * blockIdx.x + (base + t0 == p0 ? 0 : 1);
       if (f.tile0 == 0) {        // the first part: this CTA's entry for the joining kernel
         const long long last = base + tiles - 1;           // the gang that holds the last tile
-        merge_parts = static_cast<int>(div_small((last + 1) * ngangs + total - 1, total)) - gang_id;
+        merge_parts = static_cast<int>(lat_div((last + 1) * ngangs + total - 1, total)) - gang_id;
         merge_slot = f.slot;
         merge_row = f.row0;
         merge_cols = f.cols;
@@ -389,75 +347,52 @@ __device__ __forceinline__ int float_order(float x) {      // order of floats as
 __device__ __forceinline__ float order_float(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
 
 // One of a thread's columns chosen by a runtime index, without indexing registers.
-template <int C>
-__device__ __forceinline__ float pick(const float (&v)[C], int i) {
+__device__ __forceinline__ float pick8(const float (&v)[8], int i) {
   float x = v[0];
 #pragma unroll
-  for (int c = 1; c < C; ++c) x = i == c ? v[c] : x;
+  for (int c = 1; c < 8; ++c) x = i == c ? v[c] : x;
   return x;
 }
 
-// A thread's share of its warpgroup's query columns: 128 / C threads per column, 9 pieces of C / 2
-// bf16 entries each. Loaded while the fragment before is written out.
+// A thread's share of its warpgroup's 8 query columns: 16 threads per column, 9 pieces of 4 entries
+// each. Loaded while the fragment before is still being worked on.
 template <int HG>
 struct LatQueries {
-  static constexpr int C = LatSmem<HG>::kCols, kPer = 128 / C, kWords = C / 4;
-  uint32_t x[9][kWords];
+  uint2 x[9];
 
   __device__ __forceinline__ void load(const LatAttnArgs& a, const LatFragment& f, int group, int tid) {
-    const int c = group * C + tid / kPer;
+    const int c = group * 8 + (tid >> 4);
     // a column without a query repeats the fragment's first one: its result is not written
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(
-        a.q + (static_cast<size_t>(f.row0) + (c < f.cols ? c : 0)) * kLatDk) + tid % kPer * kWords;
+    const uint2* src =
+        reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(f.row0) + (c < f.cols ? c : 0)) * kLatDk) + (tid & 15);
 #pragma unroll
-    for (int j = 0; j < 9; ++j) {
-      if constexpr (kWords == 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + j * kPer * 4));
-        x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
-      } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + j * kPer * 2));
-        x[j][0] = v.x, x[j][1] = v.y;
-      }
-    }
+    for (int j = 0; j < 9; ++j) x[j] = __ldg(src + j * 16);
   }
 
   // Splits the entries into their two terms and stores them as the score MMAs' B operand: core
-  // matrices of 8 rows x 16 bytes, this group's rows being its C high terms, then its C low ones.
-  // Returns the scale of column tid / kPer: NaN for a row with an entry that is not finite, which makes
+  // matrices of 8 rows x 16 bytes, this group's rows being its 8 high terms, then its 8 low ones.
+  // Returns the scale of column tid / 16: NaN for a row with an entry that is not finite, which makes
   // all its scores NaN whatever its codes are.
   __device__ __forceinline__ float store(uint8_t* qs, int group, int tid) const {
     constexpr int kLead = LatSmem<HG>::kQRows * 16;        // from 16 entries to the next
     uint32_t mx = 0;
 #pragma unroll
-    for (int j = 0; j < 9; ++j)
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) mx = __vmaxu2(mx, x[j][i] & 0x7fff7fffu);
+    for (int j = 0; j < 9; ++j) mx = __vmaxu2(mx, __vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu));
     mx = max(mx & 0xffffu, mx >> 16);
-    for (int d = 1; d < kPer; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    for (int d = 1; d < 16; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     const int ex = max(kScaleMinExp, static_cast<int>(mx >> 7) - 135 + ((mx & 0x7fu) > 96u ? 1 : 0));
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
     const __half2 k16 = __float2half2_rn(16.0f);
-    const int at = tid % kPer * kWords * 2;                // this thread's entries of each kPer * C / 2
-    uint8_t* dst = qs + (at >> 4) * kLead + (at & 15) + (group * 2 * C + tid / kPer) * 16;
+    uint8_t* dst = qs + ((tid & 15) >> 2) * kLead + (tid & 3) * 4 + (group * 16 + (tid >> 4)) * 16;
 #pragma unroll
     for (int j = 0; j < 9; ++j, dst += 4 * kLead) {        // 64 entries on
-      uint32_t hi[kWords / 2], lo[kWords / 2];
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const float2 v = bf16x2_to_float(x[j][i]);
-        const __half2 h = __floats2half2_rn(v.x * inv, v.y * inv);     // at most 448: exact above 2^-16
-        const uint32_t a = half2_to_e4m3x2(h);
-        const uint32_t b = half2_to_e4m3x2(__hmul2(__hsub2(h, e4m3x2_to_half2(static_cast<uint16_t>(a))), k16));
-        hi[i / 2] = i % 2 ? hi[i / 2] | a << 16 : a;
-        lo[i / 2] = i % 2 ? lo[i / 2] | b << 16 : b;
-      }
-      if constexpr (kWords == 4) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(dst + C * 16) = make_uint2(lo[0], lo[1]);
-      } else {
-        *reinterpret_cast<uint32_t*>(dst) = hi[0];
-        *reinterpret_cast<uint32_t*>(dst + C * 16) = lo[0];
-      }
+      const float2 v0 = bf16x2_to_float(x[j].x), v1 = bf16x2_to_float(x[j].y);
+      const __half2 h0 = __floats2half2_rn(v0.x * inv, v0.y * inv), h1 = __floats2half2_rn(v1.x * inv, v1.y * inv);
+      const uint16_t hi0 = half2_to_e4m3x2(h0), hi1 = half2_to_e4m3x2(h1);         // at most 448: h exact above 2^-16
+      const uint16_t lo0 = half2_to_e4m3x2(__hmul2(__hsub2(h0, e4m3x2_to_half2(hi0)), k16));
+      const uint16_t lo1 = half2_to_e4m3x2(__hmul2(__hsub2(h1, e4m3x2_to_half2(hi1)), k16));
+      *reinterpret_cast<uint32_t*>(dst) = hi0 | (static_cast<uint32_t>(hi1) << 16);
+      *reinterpret_cast<uint32_t*>(dst + 128) = lo0 | (static_cast<uint32_t>(lo1) << 16);
     }
     return mx >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
   }
@@ -467,20 +402,15 @@ template <int HG>
 __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename LatSmem<HG>::Info* s, uint8_t* smem,
                                                  uint32_t tmem) {
   using SM = LatSmem<HG>;
-  constexpr int C = SM::kCols;
   volatile int* abort_flag = &s->abort;
-  const int tid = threadIdx.x & 127, group = (threadIdx.x >> 7) - 1;   // warpgroup of C columns
+  const int tid = threadIdx.x & 127, group = (threadIdx.x >> 7) - 1;   // warpgroup of 8 columns
   const int warp = tid >> 5, lane = tid & 31;
   const int bar_id = 1 + group;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-  // N columns of the weights' terms, in blocks of 16: hi, lo, lo2 of each group of 16 columns; or, of two
-  // groups of 8, hi and lo of the first, both lo2, hi and lo of the second.
-  const int block = C == 16 ? 3 * group : 3 * (group >> 1) + 2 * (group & 1), block2 = C == 16 ? block + 2 : 3 * (group >> 1) + 1, at2 = C == 16 ? 0 : 8 * (group & 1);
-  const uint32_t acc1 = lane_base + SM::kTmemO + 16 * block, acc2 = lane_base + SM::kTmemO + 16 * block2 + at2;
-  auto load_acc = [&](int m, float (&x)[3 * C]) {          // hi, lo and lo2 sums of 128 value columns
-    if constexpr (C == 16) tmem_load_32_16(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
-    else tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
-  };
+  // The terms of two groups' weights share 48 N columns: hi and lo of the first, both lo2, hi and lo
+  // of the second; 16 bytes of a token's weights are one block of 16 N columns.
+  const int block = 3 * (group >> 1) + 2 * (group & 1), block2 = 3 * (group >> 1) + 1, half8 = 8 * (group & 1);
+  const uint32_t acc1 = lane_base + SM::kTmemO + 16 * block, acc2 = lane_base + SM::kTmemO + 16 * block2 + half8;
   const float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   const bool capped = a.logit_cap > 0.0f;
   // cap * tanh(t / cap) * log2(e) = cap2 - 2 cap2 / (1 + 2^(t cap_in)): off by a few 2^-24 of the cap
@@ -490,9 +420,11 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
   uint32_t fphase = 0;
   int it = 0;                                              // tiles so far: buffers and phases follow it
   int turn = 0;                                            // it % 3
+  int nfrag = 0;
   LatFragment f;
-  LatQueries<HG> queries;
   bool ok;
+  // The next fragment, its queries split and handed to the score MMAs. The MMAs of the fragment before
+  // are done with theirs (its last s_full was waited for), and its accumulators are not concerned.
   auto next_fragment = [&](LatFragment& to) {
     ok = lat_wait(&s->frag_full[fslot], fphase, abort_flag);
     if (group_any(bar_id, !ok)) return false;
@@ -500,57 +432,56 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     __syncwarp();
     if (lane == 0) mbar_arrive(&s->frag_empty[fslot]);
     if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
-    if (to.valid) queries.load(a, to, group, tid);
+    if (!to.valid) return true;
+    LatQueries<HG> queries;
+    queries.load(a, to, group, tid);
+    const float qscale = queries.store(smem + SM::kOffQ, group, tid);
+    if ((tid & 15) == 0) s->qfac[nfrag & 1][group][tid >> 4] = qscale * (a.sm_scale * (capped ? 1.0f : kLog2e));
+    ++nfrag;
+    fence_proxy_async_smem();
+    group_sync(bar_id);
+    if (tid == 0) mbar_arrive(&s->q_full);
     return true;
   };
   if (!next_fragment(f)) return false;
   while (f.valid) {
-    // The earlier fragment's score MMAs are done (its last s_full was waited for): their operand
-    // may be overwritten.
-    const float qscale = queries.store(smem + SM::kOffQ, group, tid);
-    if (tid % (128 / C) == 0) s->inv[group][tid / (128 / C)] = qscale * (a.sm_scale * (capped ? 1.0f : kLog2e));
-    fence_proxy_async_smem();
-    group_sync(bar_id);
-    if (tid == 0) mbar_arrive(&s->q_full);
-    float fac[C], nref[C], sum[C];                         // nref: code exponent of the reference minus the reference
+    float fac[8], nref[8], sum[8];                         // nref: code exponent of the reference minus the reference
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      fac[c] = s->inv[group][c];
+    for (int c = 0; c < 8; ++c) {
+      fac[c] = s->qfac[(nfrag - 1) & 1][group][c];
       nref[c] = kLatNoRef;
       sum[c] = 0.0f;
     }
     const float ref_exp = lat_ref_exponent(f.len);
-    const int query = (f.col0 + group * C) / a.Hq;
+    const int query = a.Hq >= f.col0 + HG ? 0 : (f.col0 + group * 8) / a.Hq;
     const int sees_min = f.sees0 + query;                  // of this group's first column
-    const int next_query = (query + 1) * a.Hq - (f.col0 + group * C);  // columns until the next query
+    const int next_query = (query + 1) * a.Hq - (f.col0 + group * 8);  // columns until the next query
 
     for (int tile = f.tile0; tile < f.tile1; ++tile, ++it, turn = turn == 2 ? 0 : turn + 1) {
       const int buf = it & 1;
       const uint32_t phase = (it >> 1) & 1;
       const int ahead = it % kLatAhead;
-      ok = lat_wait(&s->tab_full[ahead], (it / kLatAhead) & 1, abort_flag);
+      ok = lat_wait(&s->scale_full[ahead], (it / kLatAhead) & 1, abort_flag);
       const float sc = s->scale[ahead][tid];
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->tab_empty[ahead]);
       // the reference of a column bounds score + log2(page scale): the weights that meet the codes
       const float bound = kLatTopExp - (sc > 0.0f ? __log2f(sc) : -100.0f);
-      float2 fs[C / 2];
+      float2 fs[4];
 #pragma unroll
-      for (int i = 0; i < C / 2; ++i) fs[i] = make_float2(fac[2 * i] * sc, fac[2 * i + 1] * sc);
+      for (int i = 0; i < 4; ++i) fs[i] = make_float2(fac[2 * i] * sc, fac[2 * i + 1] * sc);
       ok = lat_wait(&s->s_full[buf], phase, abort_flag) && ok;
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      float t[C];
+      float t[8];
       {
-        float v[2 * C];
-        const uint32_t at = lane_base + SM::kTmemS + buf * SM::kQRows + group * 2 * C;
-        if constexpr (C == 16) tmem_load_32(at, v);
-        else tmem_load_16(at, v);
+        float v[16];
+        tmem_load_16(lane_base + SM::kTmemS + buf * SM::kQRows + group * 16, v);
         tc_fence_before();
         if (lane == 0) mbar_arrive(&s->s_empty[buf]);
 #pragma unroll
-        for (int i = 0; i < C / 2; ++i) {
-          const float2 x = __fmul2_rn(__ffma2_rn(make_float2(v[C + 2 * i], v[C + 1 + 2 * i]), make_float2(0.0625f, 0.0625f),
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = __fmul2_rn(__ffma2_rn(make_float2(v[8 + 2 * i], v[9 + 2 * i]), make_float2(0.0625f, 0.0625f),
                                                  make_float2(v[2 * i], v[2 * i + 1])),
                                       fs[i]);
           t[2 * i] = x.x;
@@ -561,39 +492,75 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       if (isnan(t[0])) {
         bad = true;
 #pragma unroll
-        for (int c = 1; c < C; ++c) bad = bad && isnan(t[c]);
+        for (int c = 1; c < 8; ++c) bad = bad && isnan(t[c]);
       }
       if (capped) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) t[c] = cap2 - 2.0f * cap2 * __fdividef(1.0f, 1.0f + exp2_fast(t[c] * cap_in));
+        for (int c = 0; c < 8; ++c) t[c] = cap2 - 2.0f * cap2 * __fdividef(1.0f, 1.0f + exp2_fast(t[c] * cap_in));
       }
       const int pos = tile * kLatTile + tid;
       if ((tile + 1) * kLatTile > min(sees_min, f.len)) {
         int sees = sees_min, left = next_query;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
+        for (int c = 0; c < 8; ++c) {
           if (pos >= min(sees, f.len)) t[c] = -INFINITY;
           if (--left == 0) { left = a.Hq; ++sees; }
         }
       }
-      // the weights' exponents, and whether one passes its bound (fmaxf passes over NaN; a column that
-      // has no reference yet raises the flag with its first finite score)
-      float w[C], top = -INFINITY;
+      // A score that passes its bound raises a flag, which is read after the barrier below; until then
+      // the weights are computed as if there were none. A fragment's first tile has no references yet:
+      // it takes them first. (fmaxf passes over NaN.)
+      bool moves = tile == f.tile0;
+      float w[8], top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
+      for (int c = 0; c < 8; ++c) {
         w[c] = t[c] + nref[c];
         top = fmaxf(top, w[c]);
       }
-      // A raised flag is read after the barrier below; until then the weights are computed as if there
-      // were none.
-      if (!ok) flag[turn] = 2;
-      else if (top > bound) atomicOr(const_cast<int*>(&flag[turn]), 1);
-      uint32_t hi[C / 4], lo[C / 4], lo2[C / 4];
-      for (bool again = false;; again = true) {
+      if (!moves && top > bound) atomicOr(const_cast<int*>(&flag[turn]), 1);
+      if (!ok) atomicOr(const_cast<int*>(&flag[turn]), 2);
+      uint32_t hi[2], lo[2], lo2[2];
+      for (;;) {
+        if (moves) {
+          // new references: the largest over the tile, where that is larger
+          const float lg = kLatTopExp - bound;
 #pragma unroll
-        for (int c = 0; c < C; ++c) w[c] = exp2_fast(w[c]);
+          for (int c = 0; c < 8; ++c) {
+            const float x = isnan(t[c]) ? -INFINITY : t[c] + lg;
+            const int m = __reduce_max_sync(0xffffffffu, float_order(x));
+            if (lane == 0) s->red[group][warp][c] = order_float(m);
+          }
+          ok = (tile == f.tile0 || lat_wait(&s->p_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort_flag)) && ok;
+          if (group_any(bar_id, !ok)) return false;
+          float alpha[8];
 #pragma unroll
-        for (int i = 0; i < C / 4; ++i) {
+          for (int c = 0; c < 8; ++c) {
+            const float m = fmaxf(fmaxf(s->red[group][0][c], s->red[group][1][c]),
+                                  fmaxf(s->red[group][2][c], s->red[group][3][c]));
+            const float next = fminf(nref[c], ref_exp - m);            // m = -inf: as it was
+            alpha[c] = exp2_fast(next - nref[c]);
+            nref[c] = next;
+            sum[c] *= alpha[c];
+            w[c] = t[c] + next;
+          }
+          if (tile > f.tile0) {                            // what has been summed, in the new references
+            tc_fence_after();
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {
+              float x[24];
+              tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
+#pragma unroll
+              for (int i = 0; i < 24; ++i) x[i] *= alpha[i & 7];
+              tmem_store_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = exp2_fast(w[c]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           uint16_t h[2], l[2], l2[2];
           split_weights(w[4 * i] * sc, w[4 * i + 1] * sc, h[0], l[0], l2[0]);
           split_weights(w[4 * i + 2] * sc, w[4 * i + 3] * sc, h[1], l[1], l2[1]);
@@ -601,61 +568,19 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
           lo[i] = l[0] | (static_cast<uint32_t>(l[1]) << 16);
           lo2[i] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
         }
-        if (again) break;
         ok = lat_wait(&s->p_empty[buf], phase ^ 1u, abort_flag);       // the P V two tiles ago is done
-        if (!ok) flag[turn] = 2;
-        group_sync(bar_id);
+        if (!ok) atomicOr(const_cast<int*>(&flag[turn]), 2);
+        group_sync(bar_id);                                // (red, too, may be written again after it)
         const int raised = flag[turn];
         if (raised & 2) return false;
-        if (!raised) break;
-        // new references: the largest over the tile, where that is larger
-        const float lg = kLatTopExp - bound;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float x = isnan(t[c]) ? -INFINITY : t[c] + lg;
-          const int m = __reduce_max_sync(0xffffffffu, float_order(x));
-          if (lane == 0) s->red[group][warp][c] = order_float(m);
-        }
-        ok = tile == f.tile0 || lat_wait(&s->p_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort_flag);
-        if (group_any(bar_id, !ok)) return false;
-        float alpha[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float m = fmaxf(fmaxf(s->red[group][0][c], s->red[group][1][c]),
-                                fmaxf(s->red[group][2][c], s->red[group][3][c]));
-          const float next = fminf(nref[c], ref_exp - m); // m = -inf: as it was
-          alpha[c] = exp2_fast(next - nref[c]);
-          nref[c] = next;
-          sum[c] *= alpha[c];
-          w[c] = t[c] + next;
-        }
-        if (tile > f.tile0) {                              // what has been summed, in the new references
-          tc_fence_after();
-#pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            float x[3 * C];
-            load_acc(m, x);
-#pragma unroll
-            for (int i = 0; i < 3 * C; ++i) x[i] *= alpha[i & (C - 1)];
-            if constexpr (C == 16) tmem_store_32_16(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
-            else tmem_store_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-        }
-        group_sync(bar_id);                                // red may be written again
+        if (moves || !raised) break;
+        moves = true;
       }
       // the flag of the tile after the next: read before this barrier, raised after the next one
       if (tid == 0) flag[turn == 0 ? 2 : turn - 1] = 0;
       uint8_t* pb = smem + SM::kOffP + buf * SM::kPBytes + tid * 16;
-      if constexpr (C == 16) {
-        *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(pb + (block + 1) * (16 * kLatTile)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(pb + block2 * (16 * kLatTile)) = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
-      } else {
-        *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-        *reinterpret_cast<uint2*>(pb + block2 * (16 * kLatTile) + at2) = make_uint2(lo2[0], lo2[1]);
-      }
+      *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(pb + block2 * (16 * kLatTile) + half8) = make_uint2(lo2[0], lo2[1]);
       if (bad) {
         // the row must not reach columns that give it no weight (0 x NaN): its values become 0, the
         // weights of the columns that do see it are NaN themselves
@@ -668,58 +593,65 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->p_full[buf]);
 #pragma unroll
-      for (int c = 0; c < C; ++c) sum[c] += w[c];
+      for (int c = 0; c < 8; ++c) sum[c] += w[c];
     }
 
-    // ---- the fragment's result: the columns' sums over all threads, then the accumulators; the next
-    // fragment's queries are on their way meanwhile
+    // ---- the next fragment's queries, so that its first scores are on their way; then this one's result:
+    // the columns' sums over all threads, and the accumulators
     LatFragment next;
     if (!next_fragment(next)) return false;
     ok = lat_wait(&s->p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag);
-    // each of the upper lane bits chooses a half of the columns: 32 / C lanes end with parts of one column's sum
-    constexpr int kShare = 32 / C;
+    // lane bits 4 .. 2 choose a half of the columns each: four lanes end with parts of one column's sum
 #pragma unroll
-    for (int h = C / 2; h; h >>= 1) {
-      const bool upper = (lane & (kShare * h)) != 0;
+    for (int h = 4; h; h >>= 1) {
+      const bool upper = (lane & (4 * h)) != 0;
 #pragma unroll
       for (int c = 0; c < h; ++c) {
         const float keep = upper ? sum[c + h] : sum[c], give = upper ? sum[c] : sum[c + h];
-        sum[c] = keep + __shfl_xor_sync(0xffffffffu, give, kShare * h);
+        sum[c] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * h);
       }
     }
-#pragma unroll
-    for (int d = kShare / 2; d; d >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
-    if (lane % kShare == 0) s->red[group][warp][lane / kShare] = sum[0];
+    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
+    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+    if ((lane & 3) == 0) s->red[group][warp][lane >> 2] = sum[0];
     if (group_any(bar_id, !ok)) return false;
     tc_fence_after();
-    const int live = min(C, f.cols - group * C);
-    const size_t row0 = static_cast<size_t>(f.row0) + group * C;
-    const size_t part0 = static_cast<size_t>(max(f.slot, 0)) * HG + group * C;
-    if (tid < C) {
+    const int live = min(8, f.cols - group * 8);
+    const size_t row0 = static_cast<size_t>(f.row0) + group * 8;
+    const size_t part0 = static_cast<size_t>(max(f.slot, 0)) * HG + group * 8;
+    if (tid < 8) {
       const float l = (s->red[group][0][tid] + s->red[group][1][tid]) + (s->red[group][2][tid] + s->red[group][3][tid]);
-      const float m = pick(nref, tid);                     // l sums 2^(score + m)
+      const float m = pick8(nref, tid);                    // l sums 2^(score + m)
       if (tid < live) {
         if (f.slot >= 0) a.part_ml[part0 + tid] = make_float2(m, l);
         else if (a.lse) a.lse[row0 + tid] = l == 0.0f ? -INFINITY : (log2f(l) - m) * kLn2;
       }
-      // what the accumulators are multiplied by: a part stays as it is
-      s->inv[group][tid] = f.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      s->inv[group][tid] = l == 0.0f ? 0.0f : 1.0f / l;
     }
     group_sync(bar_id);
+    if (f.slot < 0) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) sum[c] = s->inv[group][c];
+      for (int c = 0; c < 8; ++c) sum[c] = s->inv[group][c];
+      __nv_bfloat16* dst = a.o + row0 * kLatDv + tid;
 #pragma unroll 1
-    for (int m = 0; m < 4; ++m) {
-      float x[3 * C];
-      load_acc(m, x);
-      const int d = m * 128 + tid;
+      for (int m = 0; m < 4; ++m, dst += 128) {
+        float x[24];
+        tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float y = fmaf(fmaf(x[2 * C + c], 0.03125f, x[C + c]), 0.03125f, x[c]);
-        if (c < live) {
-          if (f.slot < 0) a.o[(row0 + c) * kLatDv + d] = __float2bfloat16(sum[c] == 0.0f ? 0.0f : y * sum[c]);
-          else a.part_o[(part0 + c) * kLatDv + d] = y;
+        for (int c = 0; c < 8; ++c) {
+          const float y = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]) * sum[c];
+          if (c < live) dst[c * kLatDv] = __float2bfloat16(sum[c] == 0.0f ? 0.0f : y);
         }
+      }
+    } else {                                               // a part, as it stands
+      float* dst = a.part_o + part0 * kLatDv + tid;
+#pragma unroll 1
+      for (int m = 0; m < 4; ++m, dst += 128) {
+        float x[24];
+        tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < live) dst[c * kLatDv] = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]);
       }
     }
     tc_fence_before();
@@ -819,9 +751,10 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
 }
 
 // ---------------------------------------------------------------- page table and row loads
-// Warp 3: the rows and scales of the tiles, some tiles ahead of their loads. A lane looks up a run
-// of rows (or four single ones) and writes four tokens' scales.
-template <int HG>
+// Warp 3: the rows and scales of the tiles, some tiles ahead of their loads. A lane looks up a box of
+// rows (SMALL: its four tokens) and hands over four tokens' scales; the rows go first, the loads do
+// not need the scales.
+template <int HG, bool SMALL>
 __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename LatSmem<HG>::Info* s) {
   volatile int* abort_flag = &s->abort;
   const int lane = threadIdx.x & 31;
@@ -834,75 +767,58 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
     __syncwarp();
     if (lane == 0) mbar_arrive(&s->frag_empty[fslot]);
     if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
-    const int tile1 = f.valid ? f.tile1 : f.tile0 + 1;      // the end takes an entry too
+    const int tile1 = f.valid ? f.tile1 : f.tile0 + 1;     // the end takes an entry too
     for (int tile = f.tile0; tile < tile1; ++tile) {
-      const int tok = tile * kLatTile;
-      int4 rows = make_int4(-1, -1, -1, -1);
-      float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (run) {
-        const int pos = tok + lane * run;
-        float one = 0.0f;
-        if (lane < kLatTile / run && pos < f.len) {
-          const int at = pos / ps, page = table_page(a.table, f.first + at);
-          if (page >= 0) {
-            rows.x = page * ps + (pos - at * ps);
-            one = __ldg(a.scale + page);
-          }
-        }
-        one = __shfl_sync(0xffffffffu, one, 4 * lane / run);
-        sc = make_float4(one, one, one, one);
-      } else {
-        const int pos = tok + 4 * lane;
-        int* r = reinterpret_cast<int*>(&rows);
-        float* c = reinterpret_cast<float*>(&sc);
-        int seen = -1;                                     // a row past the end, or of a bad page, repeats another
-        if (pos < f.len) {
-          int at = pos / ps, off = pos - at * ps;
+      const int pos = tile * kLatTile + lane * (SMALL ? 4 : run);
+      int page[SMALL ? 4 : 1], rows[SMALL ? 4 : 1];
+      int at = pos / ps, off = pos - at * ps;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int page = table_page(a.table, f.first + at);
-            if (page >= 0) {
-              r[i] = page * ps + off;
-              c[i] = __ldg(a.scale + page);
-              seen = r[i];
-            }
-            if (pos + i + 1 < f.len && ++off == ps) { off = 0; ++at; }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (r[i] < 0) r[i] = seen;
-        }
+      for (int i = 0; i < (SMALL ? 4 : 1); ++i) {
+        page[i] = -1;
+        if (pos + i < f.len && (SMALL || lane < kLatTile / run)) page[i] = table_page(a.table, f.first + at);
+        rows[i] = page[i] < 0 ? -1 : page[i] * ps + off;
+        if (++off == ps) { off = 0; ++at; }
       }
-      const int live = __popc(__ballot_sync(0xffffffffu, rows.x >= 0)) * (run ? run : 4);
       if (!__all_sync(0xffffffffu, lat_wait(&s->tab_empty[slot], phase ^ 1u, abort_flag))) return false;
-      s->rows[slot][lane] = rows;
-      *reinterpret_cast<float4*>(&s->scale[slot][4 * lane]) = sc;
+      if constexpr (SMALL) {
+        *reinterpret_cast<int4*>(&s->rows[slot][4 * lane]) = make_int4(rows[0], rows[1], rows[2], rows[3]);
+      } else {
+        s->rows[slot][lane] = rows[0];
+      }
+      const int live = SMALL ? 0 : __popc(__ballot_sync(0xffffffffu, rows[0] >= 0)) * run;
       if (lane == 0) s->live[slot] = f.valid ? live : -1;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s->tab_full[slot]);
+      if (lane == 0) mbar_arrive(&s->rows_full[slot]);
+      float sc[4];
+#pragma unroll
+      for (int i = 0; i < (SMALL ? 4 : 1); ++i) sc[i] = page[i] < 0 ? 0.0f : __ldg(a.scale + page[i]);
+      if constexpr (!SMALL) sc[0] = sc[1] = sc[2] = sc[3] = __shfl_sync(0xffffffffu, sc[0], 4 * lane / run);
+      *reinterpret_cast<float4*>(&s->scale[slot][4 * lane]) = make_float4(sc[0], sc[1], sc[2], sc[3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s->scale_full[slot]);
       if (++slot == kLatAhead) { slot = 0; phase ^= 1u; }
     }
     if (!f.valid) return true;
   }
 }
 
-// Warp 0: the loads, a half of a tile at a time as P V frees them. As in the MMA warp all lanes run
-// the loop and one issues: 43 cycles per copy, 100 to 150 from a divergent branch.
+// Warp 0, pages of 32 rows and more: TMA boxes, a half of a tile at a time as P V frees them. As in
+// the MMA warp all lanes run the loop and one issues: a copy takes 80 cycles to issue, 100 to 150 from
+// a divergent branch.
 template <int HG>
 __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtensorMap* tm_lat, const CUtensorMap* tm_rot,
-                                              typename LatSmem<HG>::Info* s, uint8_t* smem_any) {
+                                              typename LatSmem<HG>::Info* s, uint8_t* smem) {
   using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
-  uint8_t* smem = smem_any;
-  const int run = a.run, step = run ? run : 4, pieces = kLatTile / step;
+  const int run = a.run, pieces = kLatTile / run;
   for (int it = 0;; ++it) {
     const int ahead = it % kLatAhead;
-    if (!__all_sync(0xffffffffu, lat_wait(&s->tab_full[ahead], (it / kLatAhead) & 1, abort_flag))) return false;
+    if (!__all_sync(0xffffffffu, lat_wait(&s->rows_full[ahead], (it / kLatAhead) & 1, abort_flag))) return false;
     const int live = __shfl_sync(0xffffffffu, s->live[ahead], 0);
     if (live < 0) return true;
-    const int4 mine = s->rows[ahead][lane];
+    const int mine = s->rows[ahead][lane];
     uint8_t* rot = smem + SM::kOffRot + it % SM::kRots * kLatRot;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {                 // rotary entries and chunks 0, 1; chunks 2, 3
@@ -911,26 +827,13 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
       uint8_t* dst = smem + h.slot * kLatHalf;
       if (!__all_sync(0xffffffffu, lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag))) return false;
       if (leader) mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
-      if (run) {
 #pragma unroll 1
-        for (int i = 0, at = 0; i < pieces; ++i, at += step) {
-          const int row = __shfl_sync(0xffffffffu, mine.x, i);
-          if (row >= 0 && leader) {
-            if (half == 0) tma_load_2d(rot + at * 64, tm_rot, full, 512, row);
-            tma_load_2d(dst + at * 128, tm_lat, full, half * 256, row);
-            tma_load_2d(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, row);
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (int i = 0, at = 0; i < pieces; ++i, at += step) {
-          const int4 rows = make_int4(__shfl_sync(0xffffffffu, mine.x, i), __shfl_sync(0xffffffffu, mine.y, i),
-                                      __shfl_sync(0xffffffffu, mine.z, i), __shfl_sync(0xffffffffu, mine.w, i));
-          if (rows.x >= 0 && leader) {
-            if (half == 0) tma_gather4(rot + at * 64, tm_rot, full, 512, rows);
-            tma_gather4(dst + at * 128, tm_lat, full, half * 256, rows);
-            tma_gather4(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, rows);
-          }
+      for (int i = 0, at = 0; i < pieces; ++i, at += run) {
+        const int row = __shfl_sync(0xffffffffu, mine, i);
+        if (row >= 0 && leader) {
+          if (half == 0) tma_load_2d(rot + at * 64, tm_rot, full, 512, row);
+          tma_load_2d(dst + at * 128, tm_lat, full, half * 256, row);
+          tma_load_2d(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, row);
         }
       }
       __syncwarp();
@@ -939,12 +842,85 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
   }
 }
 
-// ---------------------------------------------------------------- the kernel
+// Four warps, smaller pages: 16-byte asynchronous copies into the places (and the swizzle) that the
+// boxes would use. A tile of single rows took 4500 cycles as TMA gathers from four warps, 40 boxes of
+// 16 rows 4400; this takes 3200 or less, about what HBM needs. A warp copies 32 rows; each of its
+// instructions 64 bytes of 8 rows.
 template <int HG>
-__global__ void __launch_bounds__(LatSmem<HG>::kThreads, 1)
+__device__ __forceinline__ bool lat_copy_role(const LatAttnArgs& a, const uint8_t* cache, typename LatSmem<HG>::Info* s,
+                                              uint8_t* smem) {
+  using SM = LatSmem<HG>;
+  volatile int* abort_flag = &s->abort;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int r8 = lane >> 2, l4 = lane & 3;                 // row of 8, 16 bytes of 64
+  const uint32_t in_tile = smem_u32(smem) + (warp * 32 + r8) * 128;
+  const uint32_t lo = (l4 ^ r8) * 16, hi = ((4 + l4) ^ r8) * 16;       // the two 64-byte parts of a 128-byte row
+  const uint32_t in_rot = smem_u32(smem) + SM::kOffRot + (warp * 32 + r8) * 64 + (l4 ^ ((r8 >> 1) & 3)) * 16;
+  int pending = -1;                                        // slot whose copies have been issued but not announced
+  auto announce = [&]() {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s->kv_full[pending]);
+    pending = -1;
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {        // announces what is pending before it has to wait
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    if (pending >= 0) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      announce();
+    }
+    return __all_sync(0xffffffffu, lat_wait(bar, parity, abort_flag)) != 0;
+  };
+  bool ok = true;
+  for (int it = 0; ok; ++it) {
+    const int ahead = it % kLatAhead;
+    ok = wait(&s->rows_full[ahead], (it / kLatAhead) & 1);
+    if (!ok || s->live[ahead] < 0) break;
+    const uint8_t* src[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int row = s->rows[ahead][warp * 32 + g * 8 + r8];
+      src[g] = row < 0 ? nullptr : cache + static_cast<size_t>(row) * kLatDk + l4 * 16;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s->tab_empty[ahead]);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
+      ok = wait(&s->kv_empty[h.slot], h.phase ^ 1u);
+      if (!ok) break;
+      const uint32_t dst = in_tile + h.slot * kLatHalf, rot = in_rot + it % SM::kRots * kLatRot;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (!src[g]) continue;
+        const uint8_t* from = src[g] + half * 256;
+        const uint32_t to = dst + g * 8 * 128;
+        cp_async_16(to + lo, from);
+        cp_async_16(to + hi, from + 64);
+        cp_async_16(to + kLatChunk + lo, from + 128);
+        cp_async_16(to + kLatChunk + hi, from + 192);
+        if (half == 0) cp_async_16(rot + g * 8 * 64, src[g] + 512);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (pending >= 0) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        announce();
+      }
+      pending = h.slot;
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (ok && pending >= 0) announce();
+  return ok;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int HG, bool SMALL>
+__global__ void __launch_bounds__(kLatThreads<HG, SMALL>, 1)
 mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rot,
                const __grid_constant__ LatAttnArgs a) {
   using SM = LatSmem<HG>;
+  constexpr int kThreads = kLatThreads<HG, SMALL>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   typename SM::Info* s = reinterpret_cast<typename SM::Info*>(smem + SM::kOffInfo);
@@ -954,7 +930,7 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < SM::kHalves; ++i) {
-      mbar_init(&s->kv_full[i], 1);
+      mbar_init(&s->kv_full[i], SMALL ? 4 : 1);
       mbar_init(&s->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -967,14 +943,17 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     }
     for (int g = 0; g < kGroups; ++g) s->flag[g][0] = s->flag[g][1] = s->flag[g][2] = 0;
     for (int i = 0; i < kLatAhead; ++i) {
-      mbar_init(&s->tab_full[i], 1);
-      mbar_init(&s->tab_empty[i], 1 + 4 * kGroups);
+      mbar_init(&s->rows_full[i], 1);
+      mbar_init(&s->scale_full[i], 1);
+      mbar_init(&s->tab_empty[i], (SMALL ? 4 : 1) + 4 * kGroups);
     }
     mbar_init(&s->q_full, kGroups);
     s->abort = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tm_lat);
-    prefetch_tensormap(&tm_rot);
+    if constexpr (!SMALL) {
+      prefetch_tensormap(&tm_lat);
+      prefetch_tensormap(&tm_rot);
+    }
   }
   if (warp == 2) {
     tmem_alloc(&s->tmem, SM::kTmemCols);
@@ -982,7 +961,7 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   }
   // the work list's length, and the sequence that this CTA's share begins in: a run of
   // sequences per thread, then a scan over the threads
-  const int per = (a.table.B + SM::kThreads - 1) / SM::kThreads;
+  const int per = (a.table.B + kThreads - 1) / kThreads;
   const int b0 = threadIdx.x * per, b1 = min(a.table.B, b0 + per);
   long long mine = 0;
   LatShape sh{};
@@ -1000,7 +979,7 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   __syncthreads();
   tc_fence_after();
   long long before = incl - mine, total = 0;
-  for (int w = 0; w < SM::kThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s->scan[w];
     total += s->scan[w];
   }
@@ -1009,8 +988,8 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   const bool works = gang_id < ngangs;
   long long p0 = 0, p1 = 0;
   if (works) {
-    p0 = div_small(total * gang_id, ngangs);
-    if (warp == 2) p1 = div_small(total * (gang_id + 1), ngangs);
+    p0 = lat_div(total * gang_id, ngangs);
+    if (warp == 2) p1 = lat_div(total * (gang_id + 1), ngangs);
     if (p0 >= before && p0 < before + mine) {
       long long off = before;
       for (int b = b0; b < b1; ++b) {
@@ -1032,6 +1011,8 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   bool ok = true;
   if (!works) {
     if (threadIdx.x == 0) a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);
+  } else if (SMALL && warp >= 4 + 4 * kGroups) {
+    ok = lat_copy_role<HG>(a, a.cache, s, smem);
   } else if (warp >= 4) {
     ok = lat_softmax_role<HG>(a, s, smem, tmem);
   } else if (warp == 2) {
@@ -1040,8 +1021,8 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   } else if (warp == 1) {
     ok = lat_mma_role<HG>(s, smem, tmem);
   } else if (warp == 3) {
-    ok = lat_table_role<HG>(a, s);
-  } else {
+    ok = lat_table_role<HG, SMALL>(a, s);
+  } else if constexpr (!SMALL) {
     ok = lat_load_role<HG>(a, &tm_lat, &tm_rot, s, smem);
     if (!ok) {
       // copies already in flight must land before the CTA's shared memory goes away
