@@ -19,12 +19,11 @@
 // i.e. per TMEM lane) multiply the scores, and the weights before they are split.
 //
 // A CTA holds `HG` columns and walks 128-token tiles through a ring of half tiles in shared memory:
-//   warp 3      page table: the tiles' rows and scales, some tiles ahead
-//   warp 0      TMA: boxes of 32 to 128 rows that a page holds together, half a tile at a time
+//   warp 3      the work list (below) and the page table: the tiles' rows and scales, some tiles ahead
+//   warps 0, 2  TMA: boxes of 16 to 128 rows that a page holds together; one half of a tile each
 //   warps 12-15 for smaller pages instead: 16-byte asynchronous copies
 //   warp 1      the MMAs: scores of the next tile are issued ahead of this tile's P V if its
 //               rows have landed, else after
-//   warp 2      the work list (below), TMEM
 //   warps 4..   one warpgroup per 8 columns, a token per thread: online softmax. The running
 //               reference of a column only moves when a score passes it by more than one
 //               (base 2), and then the accumulators in TMEM are rescaled.
@@ -69,7 +68,7 @@ struct LatAttnArgs {
   float2* part_ml;               // [2 * CTAs, HG]: reference and sum
   int4* merge;                   // [CTAs]: first row, columns, parts, first part's slot (parts 0: nothing)
   int num_q, Hq, gang_log;       // CTAs of a gang: 1, 2 or 4
-  int run;                       // rows per TMA box: 32, 64 or 128
+  int run;                       // rows per TMA box: 16 to 128
   float sm_scale, logit_cap;
 };
 
@@ -268,65 +267,56 @@ __device__ __forceinline__ long long lat_div(long long a, long long b) {
   return lat_div_large(a, b);
 }
 
-// Warp 2, one lane: the fragments of positions [p0, p1) of the work list, through the ring.
+// The fragments of positions [p, p1) of the work list, one at a time.
 template <int HG>
-__device__ __forceinline__ bool lat_schedule(const LatAttnArgs& a, typename LatSmem<HG>::Info* s, long long total,
-                                             int ngangs, int gang_id, int rank, long long p0, long long p1) {
-  int b = s->start_b;
-  long long off = s->start_off;
-  LatShape sh = s->start;
-  int slot = 0, merge_parts = 0, merge_slot = 0, merge_row = 0, merge_cols = 0;
-  uint32_t phase = 0;
-  auto push = [&](const LatFragment& f) {
-    if (!mbar_wait_idle(&s->frag_empty[slot], phase ^ 1u, &s->abort)) return false;
-    s->frag[slot] = f;
-    mbar_arrive(&s->frag_full[slot]);
-    if (++slot == 2) { slot = 0; phase ^= 1u; }
-    return true;
-  };
-  for (long long p = p0; p < p1;) {
-    while (p >= off + static_cast<long long>(sh.groups) * sh.tiles) {
-      off += static_cast<long long>(sh.groups) * sh.tiles;
-      sh = lat_shape(a, ++b, HG);
-    }
-    const int v = sh.groups == 1 ? 0 : static_cast<int>(lat_div(p - off, sh.tiles));
-    const long long base = off + static_cast<long long>(v) * sh.tiles;
-    const int t0 = static_cast<int>(p - base);
-    const int t1 = static_cast<int>(min(static_cast<long long>(sh.tiles), p1 - base));
-    // early and late column groups in turn: what a causal mask takes from one share it takes from all
-    const int g = (v & 1) ? sh.groups - 1 - v / 2 : v / 2;
-    const int u = (g << a.gang_log) + rank;
-    p = base + t1;
-    if (u >= sh.units) continue;
+struct LatSchedule {
+  LatShape sh;                   // of sequence b, whose share of the list begins at off
+  int b;
+  long long off, p, p0, p1, total;
+  int ngangs, gang_id, rank;
+  int4 merge;                    // this CTA's entry for the joining kernel
+
+  __device__ __forceinline__ LatFragment next(const LatAttnArgs& a) {
     LatFragment f{};
-    f.first = sh.first;
-    const int c0 = u * HG, query = sh.n == 1 ? 0 : c0 / a.Hq;
-    f.col0 = c0 - query * a.Hq;
-    f.cols = min(HG, sh.n * a.Hq - c0);
-    f.row0 = sh.qlo * a.Hq + c0;
-    f.sees0 = sh.len - sh.n + query + 1;
-    f.len = max(0, min(sh.len, f.sees0 + (sh.n == 1 ? 0 : (f.col0 + f.cols - 1) / a.Hq)));
-    const int tiles = max(1, (f.len + kLatTile - 1) / kLatTile);
-    f.tile0 = t0;
-    f.tile1 = min(t1, tiles);
-    if (f.tile0 >= f.tile1) continue;
-    f.slot = -1;
-    f.valid = 1;
-    if (f.tile0 > 0 || f.tile1 < tiles) {
-      f.slot = 2 * blockIdx.x + (base + t0 == p0 ? 0 : 1);
-      if (f.tile0 == 0) {        // the first part: this CTA's entry for the joining kernel
-        const long long last = base + tiles - 1;           // the gang that holds the last tile
-        merge_parts = static_cast<int>(lat_div((last + 1) * ngangs + total - 1, total)) - gang_id;
-        merge_slot = f.slot;
-        merge_row = f.row0;
-        merge_cols = f.cols;
+    while (p < p1) {
+      while (p >= off + static_cast<long long>(sh.groups) * sh.tiles) {
+        off += static_cast<long long>(sh.groups) * sh.tiles;
+        sh = lat_shape(a, ++b, HG);
       }
+      const int v = sh.groups == 1 ? 0 : static_cast<int>(lat_div(p - off, sh.tiles));
+      const long long base = off + static_cast<long long>(v) * sh.tiles;
+      const int t0 = static_cast<int>(p - base);
+      const int t1 = static_cast<int>(min(static_cast<long long>(sh.tiles), p1 - base));
+      const bool begins = p == p0;
+      p = base + t1;
+      // early and late column groups in turn: what a causal mask takes from one share it takes from all
+      const int u = (((v & 1) ? sh.groups - 1 - v / 2 : v / 2) << a.gang_log) + rank;
+      if (u >= sh.units) continue;
+      const int c0 = u * HG, query = sh.n == 1 ? 0 : c0 / a.Hq;
+      f.first = sh.first;
+      f.col0 = c0 - query * a.Hq;
+      f.cols = min(HG, sh.n * a.Hq - c0);
+      f.row0 = sh.qlo * a.Hq + c0;
+      f.sees0 = sh.len - sh.n + query + 1;
+      f.len = max(0, min(sh.len, f.sees0 + (sh.n == 1 ? 0 : (f.col0 + f.cols - 1) / a.Hq)));
+      const int tiles = max(1, (f.len + kLatTile - 1) / kLatTile);
+      f.tile0 = t0;
+      f.tile1 = min(t1, tiles);
+      if (f.tile0 >= f.tile1) continue;
+      f.slot = -1;
+      f.valid = 1;
+      if (f.tile0 > 0 || f.tile1 < tiles) {
+        f.slot = 2 * blockIdx.x + (begins ? 0 : 1);
+        if (f.tile0 == 0) {      // the first part; the last tile's gang says how many there are
+          const int last_gang = static_cast<int>(lat_div((base + tiles) * ngangs + total - 1, total)) - 1;
+          merge = make_int4(f.row0, f.cols, last_gang - gang_id + 1, f.slot);
+        }
+      }
+      return f;
     }
-    if (!push(f)) return false;
+    return LatFragment{};
   }
-  a.merge[blockIdx.x] = make_int4(merge_row, merge_cols, merge_parts, merge_slot);
-  return push(LatFragment{});
-}
+};
 
 // ---------------------------------------------------------------- softmax warpgroup
 // Codes of two columns (two bytes) of the three terms of y in [0, 2^8]: y is rounded to the 11 bits
@@ -751,21 +741,25 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
 }
 
 // ---------------------------------------------------------------- page table and row loads
-// Warp 3: the rows and scales of the tiles, some tiles ahead of their loads. A lane looks up a box of
-// rows (SMALL: its four tokens) and hands over four tokens' scales; the rows go first, the loads do
-// not need the scales.
+// Warp 3: the fragments, for all roles, and the rows and scales of their tiles, some tiles ahead of
+// the loads. A lane looks up a box of rows (SMALL: its four tokens) and hands over four tokens' scales;
+// the rows go first, the loads do not need the scales.
 template <int HG, bool SMALL>
-__device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename LatSmem<HG>::Info* s) {
+__device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename LatSmem<HG>::Info* s,
+                                               LatSchedule<HG>& schedule) {
   volatile int* abort_flag = &s->abort;
   const int lane = threadIdx.x & 31;
   const int ps = a.table.page_size, run = a.run;
   int slot = 0, fslot = 0;
   uint32_t phase = 0, fphase = 0;
   for (;;) {
-    if (!__all_sync(0xffffffffu, lat_wait(&s->frag_full[fslot], fphase, abort_flag))) return false;
-    const LatFragment f = s->frag[fslot];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s->frag_empty[fslot]);
+    const LatFragment f = schedule.next(a);                // (every lane computes it)
+    if (!__all_sync(0xffffffffu, lat_wait(&s->frag_empty[fslot], fphase ^ 1u, abort_flag))) return false;
+    if (lane == 0) {
+      s->frag[fslot] = f;
+      mbar_arrive(&s->frag_full[fslot]);
+      if (!f.valid) a.merge[blockIdx.x] = schedule.merge;
+    }
     if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
     const int tile1 = f.valid ? f.tile1 : f.tile0 + 1;     // the end takes an entry too
     for (int tile = f.tile0; tile < tile1; ++tile) {
@@ -802,12 +796,13 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
   }
 }
 
-// Warp 0, pages of 32 rows and more: TMA boxes, a half of a tile at a time as P V frees them. As in
-// the MMA warp all lanes run the loop and one issues: a copy takes 80 cycles to issue, 100 to 150 from
-// a divergent branch.
+// Warps 0 and 2, pages of 16 rows and more: TMA boxes, each warp one half of every tile (half 0: the
+// rotary entries and chunks 0, 1; half 1: chunks 2, 3) as P V frees them. As in the MMA warp all lanes
+// run the loop and one issues: a copy takes 80 cycles to issue beside the softmax warps, 100 to 150
+// from a divergent branch.
 template <int HG>
 __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtensorMap* tm_lat, const CUtensorMap* tm_rot,
-                                              typename LatSmem<HG>::Info* s, uint8_t* smem) {
+                                              typename LatSmem<HG>::Info* s, uint8_t* smem, int half) {
   using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
   const int lane = threadIdx.x & 31;
@@ -819,26 +814,24 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
     const int live = __shfl_sync(0xffffffffu, s->live[ahead], 0);
     if (live < 0) return true;
     const int mine = s->rows[ahead][lane];
-    uint8_t* rot = smem + SM::kOffRot + it % SM::kRots * kLatRot;
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {                 // rotary entries and chunks 0, 1; chunks 2, 3
-      const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
-      uint64_t* full = &s->kv_full[h.slot];
-      uint8_t* dst = smem + h.slot * kLatHalf;
-      if (!__all_sync(0xffffffffu, lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag))) return false;
-      if (leader) mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
-#pragma unroll 1
-      for (int i = 0, at = 0; i < pieces; ++i, at += run) {
-        const int row = __shfl_sync(0xffffffffu, mine, i);
-        if (row >= 0 && leader) {
-          if (half == 0) tma_load_2d(rot + at * 64, tm_rot, full, 512, row);
-          tma_load_2d(dst + at * 128, tm_lat, full, half * 256, row);
-          tma_load_2d(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, row);
-        }
-      }
-      __syncwarp();
-    }
+    __syncwarp();
     if (leader) mbar_arrive(&s->tab_empty[ahead]);
+    const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
+    uint64_t* full = &s->kv_full[h.slot];
+    uint8_t* dst = smem + h.slot * kLatHalf;
+    uint8_t* rot = smem + SM::kOffRot + it % SM::kRots * kLatRot;
+    if (!__all_sync(0xffffffffu, lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag))) return false;
+    if (leader) mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
+#pragma unroll 1
+    for (int i = 0, at = 0; i < pieces; ++i, at += run) {
+      const int row = __shfl_sync(0xffffffffu, mine, i);
+      if (row >= 0 && leader) {
+        if (half == 0) tma_load_2d(rot + at * 64, tm_rot, full, 512, row);
+        tma_load_2d(dst + at * 128, tm_lat, full, half * 256, row);
+        tma_load_2d(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, row);
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -939,13 +932,13 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
       mbar_init(&s->p_full[i], 4 * kGroups);
       mbar_init(&s->p_empty[i], 1);
       mbar_init(&s->frag_full[i], 1);
-      mbar_init(&s->frag_empty[i], 2 + 4 * kGroups);
+      mbar_init(&s->frag_empty[i], 1 + 4 * kGroups);
     }
     for (int g = 0; g < kGroups; ++g) s->flag[g][0] = s->flag[g][1] = s->flag[g][2] = 0;
     for (int i = 0; i < kLatAhead; ++i) {
       mbar_init(&s->rows_full[i], 1);
       mbar_init(&s->scale_full[i], 1);
-      mbar_init(&s->tab_empty[i], (SMALL ? 4 : 1) + 4 * kGroups);
+      mbar_init(&s->tab_empty[i], (SMALL ? 4 : 2) + 4 * kGroups);
     }
     mbar_init(&s->q_full, kGroups);
     s->abort = 0;
@@ -986,23 +979,19 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   const int gang_id = blockIdx.x >> a.gang_log, rank = blockIdx.x - (gang_id << a.gang_log);
   const int ngangs = static_cast<int>(min(static_cast<long long>(gridDim.x >> a.gang_log), total));
   const bool works = gang_id < ngangs;
-  long long p0 = 0, p1 = 0;
-  if (works) {
-    p0 = lat_div(total * gang_id, ngangs);
-    if (warp == 2) p1 = lat_div(total * (gang_id + 1), ngangs);
-    if (p0 >= before && p0 < before + mine) {
-      long long off = before;
-      for (int b = b0; b < b1; ++b) {
-        if (per > 1) sh = lat_shape(a, b, HG);
-        const long long w = static_cast<long long>(sh.groups) * sh.tiles;
-        if (p0 < off + w) {
-          s->start_b = b;
-          s->start_off = off;
-          s->start = sh;
-          break;
-        }
-        off += w;
+  const long long p0 = works ? lat_div(total * gang_id, ngangs) : 0;
+  if (works && p0 >= before && p0 < before + mine) {
+    long long off = before;
+    for (int b = b0; b < b1; ++b) {
+      if (per > 1) sh = lat_shape(a, b, HG);
+      const long long w = static_cast<long long>(sh.groups) * sh.tiles;
+      if (p0 < off + w) {
+        s->start_b = b;
+        s->start_off = off;
+        s->start = sh;
+        break;
       }
+      off += w;
     }
   }
   __syncthreads();
@@ -1015,15 +1004,15 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     ok = lat_copy_role<HG>(a, a.cache, s, smem);
   } else if (warp >= 4) {
     ok = lat_softmax_role<HG>(a, s, smem, tmem);
-  } else if (warp == 2) {
-    if (lane == 0) ok = lat_schedule<HG>(a, s, total, ngangs, gang_id, rank, p0, p1);
-    __syncwarp();
   } else if (warp == 1) {
     ok = lat_mma_role<HG>(s, smem, tmem);
   } else if (warp == 3) {
-    ok = lat_table_role<HG, SMALL>(a, s);
+    LatSchedule<HG> schedule{s->start, s->start_b,  s->start_off, p0, p0, lat_div(total * (gang_id + 1), ngangs), total,
+                             ngangs,   gang_id,     rank,         make_int4(0, 0, 0, 0)};
+    ok = lat_table_role<HG, SMALL>(a, s, schedule);
+    if (!ok && lane == 0) a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);   // the joining kernel must not find old words
   } else if constexpr (!SMALL) {
-    ok = lat_load_role<HG>(a, &tm_lat, &tm_rot, s, smem);
+    ok = lat_load_role<HG>(a, &tm_lat, &tm_rot, s, smem, warp >> 1);
     if (!ok) {
       // copies already in flight must land before the CTA's shared memory goes away
       const unsigned long long t0 = global_timer_ns();
@@ -1042,47 +1031,46 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   }
 }
 
-// Joins the parts of the column groups that were cut: a warp per (CTA that holds a first part,
-// column), 16 value columns per lane; parts in order, so the same bits every time. A part holds
-// sums of 2^(score + m) and of those times values.
+// Joins the parts of the column groups that were cut: half a block per (CTA that holds a first part,
+// column), four value columns per thread, eight parts' loads in flight; parts in order, so the same
+// bits every time. A part holds sums of 2^(score + m) and of those times values.
 template <int HG>
-__global__ void __launch_bounds__(128) mla_fp8_join_kernel(const LatAttnArgs a) {
+__global__ void __launch_bounds__(256) mla_fp8_join_kernel(const LatAttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
-  const int cta = blockIdx.x, c = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, c = blockIdx.y * 2 + (threadIdx.x >> 7), col = threadIdx.x & 127;
   const int4 job = a.merge[cta];
-  if (job.z == 0 || c >= job.y) return;
+  if (c >= job.y) return;                                  // (no columns: nothing to join)
   float m = kLatNoRef, l = 0.0f;                           // reference (the largest is the least m) and sum so far
-  float acc[16];
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int kBatch = 8;
+  for (int i0 = 0; i0 < job.z; i0 += kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-#pragma unroll 2
-  for (int i = 0; i < job.z; ++i) {
-    const size_t at = static_cast<size_t>(i == 0 ? job.w : 2 * (cta + (i << a.gang_log))) * HG + c;
-    const float2 ml = a.part_ml[at];
-    float4 x[4];
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k;
+      const size_t at = static_cast<size_t>(i == 0 ? job.w : 2 * (cta + (i << a.gang_log))) * HG + c;
+      ml[k] = i < job.z ? a.part_ml[at] : make_float2(kLatNoRef, 0.0f);
+      x[k] = i < job.z ? reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[col] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[j * 32 + lane];
-    if (ml.y == 0.0f) continue;
-    const float next = fminf(m, ml.x), w0 = exp2f(next - m), w1 = exp2f(next - ml.x);
-    m = next;
-    l = l * w0 + ml.y * w1;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      acc[4 * j] = acc[4 * j] * w0 + x[j].x * w1;
-      acc[4 * j + 1] = acc[4 * j + 1] * w0 + x[j].y * w1;
-      acc[4 * j + 2] = acc[4 * j + 2] * w0 + x[j].z * w1;
-      acc[4 * j + 3] = acc[4 * j + 3] * w0 + x[j].w * w1;
+    for (int k = 0; k < kBatch; ++k) {
+      if (ml[k].y == 0.0f) continue;
+      const float next = fminf(m, ml[k].x), w0 = exp2f(next - m), w1 = exp2f(next - ml[k].x);
+      m = next;
+      l = l * w0 + ml[k].y * w1;
+      acc.x = acc.x * w0 + x[k].x * w1;
+      acc.y = acc.y * w0 + x[k].y * w1;
+      acc.z = acc.z * w0 + x[k].z * w1;
+      acc.w = acc.w * w0 + x[k].w * w1;
     }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t row = static_cast<size_t>(job.x) + c;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    __align__(8) __nv_bfloat162 y[2] = {__floats2bfloat162_rn(acc[4 * j] * inv, acc[4 * j + 1] * inv),
-                                        __floats2bfloat162_rn(acc[4 * j + 2] * inv, acc[4 * j + 3] * inv)};
-    reinterpret_cast<uint2*>(a.o + row * kLatDv)[j * 32 + lane] = *reinterpret_cast<const uint2*>(y);
-  }
-  if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : (log2f(l) - m) * 0.6931471805599453f;
+  __align__(8) __nv_bfloat162 y[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                                      __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
+  reinterpret_cast<uint2*>(a.o + row * kLatDv)[col] = *reinterpret_cast<const uint2*>(y);
+  if (a.lse && col == 0) a.lse[row] = l == 0.0f ? -INFINITY : (log2f(l) - m) * 0.6931471805599453f;
 }
 
 }  // namespace fp8moe

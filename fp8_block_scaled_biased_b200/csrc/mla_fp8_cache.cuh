@@ -86,7 +86,8 @@ struct AppendArgs {
   int T;
 };
 
-constexpr int kAppendHeld = 9;   // 16-byte pieces a thread keeps in registers between the passes
+constexpr int kAppendHeld = 10;  // rows a thread keeps its 16 bytes of in registers between the passes
+constexpr int kAppendMaxRows = 7;   // rows a CTA handles side by side: 7 * 72 = 504 threads
 
 // Two bf16 magnitudes' bit patterns, non-finite ones as 0 (their order is that of the values).
 __device__ __forceinline__ uint32_t finite_magnitudes(uint32_t v) {
@@ -94,51 +95,52 @@ __device__ __forceinline__ uint32_t finite_magnitudes(uint32_t v) {
   return v & ~__vcmpgeu2(v, 0x7f807f80u);
 }
 
+// Sequences whose entry of `indptr` plus b * slack is at most x (both grow with b): all threads of the
+// CTA count together.
+template <typename F>
+__device__ __forceinline__ int count_sequences(int B, F&& starts_by) {
+  int count = 0;
+  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    const int n = __syncthreads_count(b < B && starts_by(b));
+    count += n;
+    if (n < static_cast<int>(blockDim.x)) break;
+  }
+  return count;
+}
+
 // One CTA per (sequence, page written): the largest magnitude of the page's new rows, the page's
 // scale, the codes. Sequence b owns the CTAs from floor(append_indptr[b] / page_size) + 2b on:
 // its n tokens touch at most floor(n / page_size) + 2 pages, and the floors leave room for that.
-__global__ void __launch_bounds__(512) mla_kv_append_kernel(const AppendArgs a) {
+// A thread owns one 16-byte column of every `side`-th row. The rows are read once (held in
+// registers up to 70 rows, read again beyond), before the page itself is looked up. Bound by the
+// chain of dependent loads at decode and prompt sizes (four of them), by HBM beyond.
+__global__ void __launch_bounds__(512) mla_kv_append_kernel(const AppendArgs a, int side) {
   __shared__ uint32_t warp_max[16];
-  const int tid = threadIdx.x, nthreads = blockDim.x;
+  const int tid = threadIdx.x;
   const int ps = a.table.page_size;
-  int before = 0;                                            // sequences whose CTAs start at or before this one
-  for (int b0 = 0; b0 < a.table.B; b0 += nthreads) {
-    const int b = b0 + tid;
-    const bool in = b < a.table.B && __ldg(a.append_indptr + b) / ps + 2ll * b <= blockIdx.x;
-    const int n = __syncthreads_count(in);
-    before += n;
-    if (n < nthreads) break;
-  }
-  if (before == 0) return;
-  const int b = before - 1;
+  const int count = count_sequences(
+      a.table.B, [&](int b) { return __ldg(a.append_indptr + b) / ps + 2ll * b <= blockIdx.x; });
+  if (count == 0) return;
+  const int b = count - 1;
   const int lo = __ldg(a.append_indptr + b), hi = __ldg(a.append_indptr + b + 1);
-  if (lo < 0 || hi < lo || hi > a.T) {
-    if (tid == 0) raise_device_error(FP8MOE_DEVERR_PAGE);
-    return;
-  }
-  if (hi == lo) return;
   int first, len;
-  if (!sequence_extent(a.table, b, first, len)) return;
-  const int n = hi - lo, start = len - n;
-  if (start < 0) {
+  const bool table = sequence_extent(a.table, b, first, len);
+  if (lo < 0 || hi < lo || hi > a.T || (table && hi - lo > len)) {
     if (tid == 0) raise_device_error(FP8MOE_DEVERR_PAGE);
     return;
   }
-  const long long j = start / ps + (static_cast<long long>(blockIdx.x) - (lo / ps + 2ll * b));
+  if (!table || hi == lo) return;
+  const int start = len - (hi - lo);                         // position of the first new token
+  const int j = start / ps + static_cast<int>(blockIdx.x - (lo / ps + 2ll * b));
   if (j > (len - 1) / ps) return;
-  const int page = table_page(a.table, first + static_cast<int>(j));
-  if (page < 0) return;
-  const long long page_tok = j * ps;                         // first token position of the page
-  const int slot0 = static_cast<int>(max(0ll, start - page_tok));
-  const int rows = static_cast<int>(min(static_cast<long long>(ps), len - page_tok)) - slot0;
-  const __nv_bfloat16* src = a.kv_new + (lo + (page_tok + slot0 - start)) * a.ld;
-  const long long nvec = static_cast<long long>(rows) * kLatVec;
-  auto load = [&](long long v) {
-    const long long r = v / kLatVec;
-    return __ldg(reinterpret_cast<const uint4*>(src + r * a.ld + (v - r * kLatVec) * 8));
-  };
-
-  const float old = slot0 > 0 ? a.scale[page] : 0.0f;        // a page written from its first slot starts afresh
+  const int pos0 = max(start, j * ps);                       // (j * ps <= len - 1: no overflow)
+  const int slot0 = pos0 - j * ps;
+  const int rows = static_cast<int>(min(static_cast<long long>(len), (j + 1ll) * ps) - pos0);
+  const int r0 = tid / kLatVec, col = tid - r0 * kLatVec;
+  const bool active = r0 < side;
+  const __nv_bfloat16* src = a.kv_new + (lo + (pos0 - start) + static_cast<long long>(r0)) * a.ld + col * 8;
+  const long long step = static_cast<long long>(side) * a.ld;
   uint4 held[kAppendHeld];
   uint32_t mx = 0;
   auto take = [&](const uint4& x) {
@@ -146,18 +148,21 @@ __global__ void __launch_bounds__(512) mla_kv_append_kernel(const AppendArgs a) 
                                __vmaxu2(finite_magnitudes(x.z), finite_magnitudes(x.w))));
   };
 #pragma unroll
-  for (int i = 0; i < kAppendHeld; ++i) {
-    const long long v = tid + static_cast<long long>(i) * nthreads;
-    held[i] = v < nvec ? load(v) : make_uint4(0, 0, 0, 0);
-  }
+  for (int i = 0; i < kAppendHeld; ++i)
+    held[i] = active && r0 + i * side < rows ? __ldg(reinterpret_cast<const uint4*>(src + i * step)) : make_uint4(0, 0, 0, 0);
+  const int page = table_page(a.table, first + j);
+  if (page < 0) return;                                      // (the same for the whole CTA)
+  const float old = slot0 > 0 ? a.scale[page] : 0.0f;        // a page written from its first slot starts afresh
 #pragma unroll
   for (int i = 0; i < kAppendHeld; ++i) take(held[i]);
-  for (long long v = tid + static_cast<long long>(kAppendHeld) * nthreads; v < nvec; v += nthreads) take(load(v));
+  if (active)
+    for (int r = r0 + kAppendHeld * side; r < rows; r += side)
+      take(__ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld)));
   mx = max(mx & 0xffffu, mx >> 16);
   mx = __reduce_max_sync(0xffffffffu, mx);
   if ((tid & 31) == 0) warp_max[tid >> 5] = mx;
   __syncthreads();
-  for (int w = 0; w < nthreads / 32; ++w) mx = max(mx, warp_max[w]);
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) mx = max(mx, warp_max[w]);
 
   float s = 0.0f;
   if (mx != 0) {
@@ -168,24 +173,25 @@ __global__ void __launch_bounds__(512) mla_kv_append_kernel(const AppendArgs a) 
   if (tid == 0) a.scale[page] = s;                           // every thread read `old` before the barrier
   const float inv = s > 0.0f ? 1.0f / s : 1.0f;
   uint8_t* page_codes = a.cache + static_cast<size_t>(page) * ps * kLatDk;
-  uint8_t* dst = page_codes + static_cast<size_t>(slot0) * kLatDk;
-  auto store = [&](long long v, const uint4& x) {
+  uint8_t* dst = page_codes + static_cast<size_t>(slot0 + r0) * kLatDk + col * 8;
+  auto store = [&](int r, const uint4& x) {                  // r rows below this thread's first
     const float2 f0 = bf16x2_to_float(x.x), f1 = bf16x2_to_float(x.y), f2 = bf16x2_to_float(x.z),
                  f3 = bf16x2_to_float(x.w);
-    *reinterpret_cast<uint2*>(dst + v * 8) = make_uint2(float_to_e4m3x4(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv),
-                                                        float_to_e4m3x4(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv));
+    *reinterpret_cast<uint2*>(dst + static_cast<size_t>(r) * kLatDk) =
+        make_uint2(float_to_e4m3x4(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv),
+                   float_to_e4m3x4(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv));
   };
 #pragma unroll
-  for (int i = 0; i < kAppendHeld; ++i) {
-    const long long v = tid + static_cast<long long>(i) * nthreads;
-    if (v < nvec) store(v, held[i]);
-  }
-  for (long long v = tid + static_cast<long long>(kAppendHeld) * nthreads; v < nvec; v += nthreads) store(v, load(v));
+  for (int i = 0; i < kAppendHeld; ++i)
+    if (active && r0 + i * side < rows) store(i * side, held[i]);
+  if (active)
+    for (int r = r0 + kAppendHeld * side; r < rows; r += side)
+      store(r - r0, __ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld)));
 
   if (slot0 > 0 && old > 0.0f && s > old) {                  // the rows that were there, in the larger scale
     const float ratio = old / s;
     uint4* codes = reinterpret_cast<uint4*>(page_codes);
-    for (long long v = tid; v < static_cast<long long>(slot0) * (kLatDk / 16); v += nthreads) {
+    for (long long v = tid; v < static_cast<long long>(slot0) * (kLatDk / 16); v += blockDim.x) {
       uint4 x = codes[v];
       uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
@@ -207,25 +213,20 @@ struct GatherArgs {
   __nv_bfloat16* out;            // [T, 576], row stride ld
   long long ld;
   int T;
+  bool wide;                     // every output row begins at a multiple of 32 bytes
 };
 
 constexpr int kGatherRows = 32;
 constexpr int kGatherThreads = 256;
 
 // A CTA reads back 32 output rows: their cache rows first (a thread each), then 16 codes at a
-// time (one 16-byte load, two 16-byte stores).
+// time (one 16-byte load, one 32-byte store). Bound by HBM, of whose bytes two thirds are written.
 __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const GatherArgs a) {
   __shared__ long long row_at[kGatherRows];                  // cache row, or -1
   __shared__ float row_scale[kGatherRows];
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * kGatherRows;
-  int before = 0;                                            // sequences that start at or before row t0
-  for (int b0 = 0; b0 < a.table.B; b0 += kGatherThreads) {
-    const int b = b0 + tid;
-    const int n = __syncthreads_count(b < a.table.B && __ldg(a.out_indptr + b) <= t0);
-    before += n;
-    if (n < kGatherThreads) break;
-  }
+  const int before = count_sequences(a.table.B, [&](int b) { return __ldg(a.out_indptr + b) <= t0; });
   if (tid < kGatherRows) {
     const int t = t0 + tid;
     long long at = -1;
@@ -269,8 +270,12 @@ __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const Gat
       y[2 * i + 1] = __floats2bfloat162_rn(f.z * s, f.w * s);
     }
     uint4* dst = reinterpret_cast<uint4*>(a.out + (t0 + r) * a.ld) + 2 * c;
-    dst[0] = *reinterpret_cast<const uint4*>(&y[0]);
-    dst[1] = *reinterpret_cast<const uint4*>(&y[4]);
+    if (a.wide) {
+      st_global_v8(dst, reinterpret_cast<const uint32_t(&)[8]>(y));
+    } else {
+      dst[0] = *reinterpret_cast<const uint4*>(&y[0]);
+      dst[1] = *reinterpret_cast<const uint4*>(&y[4]);
+    }
   }
 }
 
