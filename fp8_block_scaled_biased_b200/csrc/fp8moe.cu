@@ -1187,7 +1187,7 @@ int mla_kv_append_fp8(const uint16_t* kv_new, int ld_new, const int32_t* append_
   a.scale = kv_scale;
   a.T = num_tokens;
   // Rows side by side: about eight rows for a thread, so that its loads overlap and small CTAs share an SM
-  // (16K tokens in pages of 16: 33 us with 7 rows side by side, PERF2 with 2).
+  // (16K tokens in pages of 16: 33 us with 7 rows side by side, 12 with 2).
   const int rows = std::min(page_size, (num_tokens + batch - 1) / batch);
   const int side = std::max(1, std::min(rows / 8, kAppendMaxRows));
   const unsigned ctas = static_cast<unsigned>(num_tokens / page_size + 2 * batch);

@@ -86,7 +86,7 @@ struct AppendArgs {
   int T;
 };
 
-constexpr int kAppendHeld = 10;  // rows a thread keeps its 16 bytes of in registers between the passes
+constexpr int kAppendHeld = 8;  // rows a thread keeps its 16 bytes of in registers between the passes
 constexpr int kAppendMaxRows = 7;   // rows a CTA handles side by side: 7 * 72 = 504 threads
 
 // Two bf16 magnitudes' bit patterns, non-finite ones as 0 (their order is that of the values).
@@ -113,9 +113,9 @@ __device__ __forceinline__ int count_sequences(int B, F&& starts_by) {
 // scale, the codes. Sequence b owns the CTAs from floor(append_indptr[b] / page_size) + 2b on:
 // its n tokens touch at most floor(n / page_size) + 2 pages, and the floors leave room for that.
 // A thread owns one 16-byte column of every `side`-th row. The rows are read once (held in
-// registers up to 70 rows, read again beyond), before the page itself is looked up. Bound by the
+// registers up to 8 each, read again beyond), before the page itself is looked up. Bound by the
 // chain of dependent loads at decode and prompt sizes (four of them), by HBM beyond.
-__global__ void __launch_bounds__(512) mla_kv_append_kernel(const AppendArgs a, int side) {
+__global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs a, int side) {
   __shared__ uint32_t warp_max[16];
   const int tid = threadIdx.x;
   const int ps = a.table.page_size;
