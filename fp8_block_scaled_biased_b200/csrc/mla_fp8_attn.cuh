@@ -42,7 +42,6 @@ namespace fp8moe {
 
 constexpr int kLatDv = 512;
 constexpr int kLatTile = 128;                              // tokens per tile
-constexpr int kLatAhead = 4;                               // tiles whose page-table entries are fetched ahead
 constexpr int kLatChunk = kLatTile * 128;                  // 128 bytes of every row of a tile
 constexpr int kLatHalf = 2 * kLatChunk;                    // two chunks: what is loaded and freed together
 constexpr int kLatRot = kLatTile * 64;                     // the rotary bytes of a tile
@@ -93,14 +92,15 @@ struct LatSmem {
   static constexpr int kQRows = 2 * HG, kPRows = 3 * HG;
   static constexpr int kQBytes = kQRows * kLatDk;
   static constexpr int kPBytes = kPRows * kLatTile;
-  // Halves of tiles in flight, as many as shared memory holds beside the queries and weights: with 16
-  // columns 2.5 tiles (an 8K decode batch took 78 us with 2), with 32 columns 2 tiles. Half 0 of a tile
-  // brings its rotary bytes along; they are free once the tile three (two) before has gone.
-  static constexpr int kHalves = HG == 16 ? 5 : 4, kRots = HG == 16 ? 3 : 2;
+  // What shared memory holds: 2.5 tiles in halves (with 2, 64 x 8192 tokens on 16 heads took 78 us
+  // instead of 73, and chunks of 500 queries on 16 heads 223 instead of PERF3), the rotary bytes of two,
+  // the queries' terms, and the weights of two tiles, or of one beside 32 columns' queries.
+  static constexpr int kHalves = 5, kRots = 2, kPBufs = HG == 16 ? 2 : 1;
+  static constexpr int kAhead = HG == 16 ? 4 : 2;          // tiles whose page-table entries are fetched ahead
   static constexpr int kOffRot = kHalves * kLatHalf;
   static constexpr int kOffQ = kOffRot + kRots * kLatRot;
   static constexpr int kOffP = kOffQ + kQBytes;
-  static constexpr int kOffInfo = kOffP + 2 * kPBytes;
+  static constexpr int kOffInfo = kOffP + kPBufs * kPBytes;
   // TMEM columns: two score buffers, four accumulators of 128 value columns
   static constexpr int kTmemS = 0, kTmemO = 2 * kQRows;
   static constexpr int kTmemCols = (kTmemO + 4 * kPRows <= 256) ? 256 : 512;
@@ -108,13 +108,13 @@ struct LatSmem {
   struct Info {
     LatFragment frag[2];
     // per tile: the tokens' rows (or only those that begin a box), -1 for none; the tokens' scales
-    int rows[kLatAhead][kLatTile];
-    float scale[kLatAhead][kLatTile];
-    int live[kLatAhead];          // rows to be loaded; -1: the end of the list
-    uint64_t rows_full[kLatAhead], scale_full[kLatAhead], tab_empty[kLatAhead];
+    int rows[kAhead][HG == 16 ? kLatTile : 32];
+    float scale[kAhead][kLatTile];
+    int live[kAhead];             // rows to be loaded; -1: the end of the list
+    uint64_t rows_full[kAhead], scale_full[kAhead], tab_empty[kAhead];
     float red[kGroups][4][8], inv[kGroups][8], qfac[2][kGroups][8];
-    uint64_t kv_full[kHalves], kv_empty[kHalves];
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
+    uint64_t kv_full[kHalves], kv_empty[kHalves], rot_empty[kRots];
+    uint64_t s_full[2], s_empty[2], p_full[kPBufs], p_empty[kPBufs];
     uint64_t frag_full[2], frag_empty[2], q_full;
     int flag[kGroups][3];         // a score passed its reference's bound (1), a wait failed (2); tiles take turns
     long long scan[24];
@@ -124,7 +124,11 @@ struct LatSmem {
     uint32_t tmem;
     int abort;
   };
-  static constexpr int kBytes = kOffInfo + static_cast<int>(sizeof(Info)) + 1024;   // + alignment
+  // 1 KB to align the start, where there is room for it: dynamic shared memory starts aligned here (and
+  // the kernel checks)
+  static constexpr int kLimit = 227 * 1024, kUsed = kOffInfo + static_cast<int>(sizeof(Info));
+  static constexpr int kBytes = kUsed + 1024 <= kLimit ? kUsed + 1024 : kLimit;
+  static_assert(kUsed <= kLimit, "shared memory of a CTA");
 };
 
 template <int HG, bool SMALL>
@@ -448,10 +452,10 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     const int next_query = (query + 1) * a.Hq - (f.col0 + group * 8);  // columns until the next query
 
     for (int tile = f.tile0; tile < f.tile1; ++tile, ++it, turn = turn == 2 ? 0 : turn + 1) {
-      const int buf = it & 1;
+      const int buf = it & 1, pbuf = it % SM::kPBufs;
       const uint32_t phase = (it >> 1) & 1;
-      const int ahead = it % kLatAhead;
-      ok = lat_wait(&s->scale_full[ahead], (it / kLatAhead) & 1, abort_flag);
+      const int ahead = it % SM::kAhead;
+      ok = lat_wait(&s->scale_full[ahead], (it / SM::kAhead) & 1, abort_flag);
       const float sc = s->scale[ahead][tid];
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->tab_empty[ahead]);
@@ -520,7 +524,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
             const int m = __reduce_max_sync(0xffffffffu, float_order(x));
             if (lane == 0) s->red[group][warp][c] = order_float(m);
           }
-          ok = (tile == f.tile0 || lat_wait(&s->p_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort_flag)) && ok;
+          ok = (tile == f.tile0 || lat_wait(&s->p_empty[(it - 1) % SM::kPBufs], ((it - 1) / SM::kPBufs) & 1, abort_flag)) && ok;
           if (group_any(bar_id, !ok)) return false;
           float alpha[8];
 #pragma unroll
@@ -558,7 +562,8 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
           lo[i] = l[0] | (static_cast<uint32_t>(l[1]) << 16);
           lo2[i] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
         }
-        ok = lat_wait(&s->p_empty[buf], phase ^ 1u, abort_flag);       // the P V two tiles ago is done
+        // the P V that read this buffer before is done
+        ok = lat_wait(&s->p_empty[pbuf], ((it / SM::kPBufs) & 1) ^ 1u, abort_flag);
         if (!ok) atomicOr(const_cast<int*>(&flag[turn]), 2);
         group_sync(bar_id);                                // (red, too, may be written again after it)
         const int raised = flag[turn];
@@ -568,7 +573,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       }
       // the flag of the tile after the next: read before this barrier, raised after the next one
       if (tid == 0) flag[turn == 0 ? 2 : turn - 1] = 0;
-      uint8_t* pb = smem + SM::kOffP + buf * SM::kPBytes + tid * 16;
+      uint8_t* pb = smem + SM::kOffP + pbuf * SM::kPBytes + tid * 16;
       *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
       *reinterpret_cast<uint2*>(pb + block2 * (16 * kLatTile) + half8) = make_uint2(lo2[0], lo2[1]);
       if (bad) {
@@ -581,7 +586,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s->p_full[buf]);
+      if (lane == 0) mbar_arrive(&s->p_full[pbuf]);
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum[c] += w[c];
     }
@@ -590,7 +595,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     // the columns' sums over all threads, and the accumulators
     LatFragment next;
     if (!next_fragment(next)) return false;
-    ok = lat_wait(&s->p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag);
+    ok = lat_wait(&s->p_empty[(it - 1) % SM::kPBufs], ((it - 1) / SM::kPBufs) & 1, abort_flag);
     // lane bits 4 .. 2 choose a half of the columns each: four lanes end with parts of one column's sum
 #pragma unroll
     for (int h = 4; h; h >>= 1) {
@@ -655,7 +660,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
 // The whole warp runs the loop and one elected lane issues, so that descriptors stay in uniform
 // registers: 44 and 48 cycles per MMA (16 columns), 70 from a divergent branch. Every turn asks all
 // barriers that matter at once, a lane each: the halves of the next tile's rows, its score buffer,
-// this tile's weights.
+// this tile's weights. A half of a tile is scored as soon as it is there.
 template <int HG>
 __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint8_t* smem, uint32_t tmem_any) {
   using SM = LatSmem<HG>;
@@ -681,17 +686,18 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
     if (n == 0) return true;
     if (!__all_sync(0xffffffffu, lat_wait(&s->q_full, fcount & 1, abort_flag))) return false;
     ++fcount;
-    int qk = 0, pv = 0;
+    int qk = 0, pv = 0;                                    // halves of tiles scored, tiles multiplied with V
     unsigned long long t0 = 0;
     for (uint32_t spin = 0; pv < n; ++spin) {
-      const int i = it0 + qk, buf = i & 1;
-      const int j = it0 + pv, pbuf = j & 1;
-      const LatHalf mine = lat_half<SM::kHalves>(2 * i + (lane & 1));
-      uint64_t* bar = lane < 2 ? &s->kv_full[mine.slot] : lane == 2 ? &s->s_empty[buf] : &s->p_full[pbuf];
-      const uint32_t parity = lane < 2 ? mine.phase : lane == 2 ? ((i >> 1) & 1) ^ 1u : (j >> 1) & 1;
-      const uint32_t ready = __ballot_sync(0xffffffffu, mbar_test(bar, parity));
-      const bool do_qk = qk < n && qk <= pv + 1 && (ready & 7u) == 7u;
-      const bool do_pv = pv < qk && (ready & 8u) != 0;
+      const int i = it0 + (qk >> 1), buf = i & 1, half = qk & 1;
+      const int j = it0 + pv, pbuf = j % SM::kPBufs;
+      const LatHalf h = lat_half<SM::kHalves>(2 * i + half);
+      uint64_t* bar = lane == 0 ? &s->kv_full[h.slot] : lane == 1 ? &s->s_empty[buf] : &s->p_full[pbuf];
+      const uint32_t parity = lane == 0 ? h.phase : lane == 1 ? ((i >> 1) & 1) ^ 1u : (j / SM::kPBufs) & 1;
+      uint32_t ready = __ballot_sync(0xffffffffu, mbar_test(bar, parity));
+      if (half) ready |= 2u;                               // the score buffer is this tile's already
+      const bool do_qk = qk < 2 * n && qk <= 2 * pv + 3 && (ready & 3u) == 3u;
+      const bool do_pv = 2 * pv + 2 <= qk && (ready & 4u) != 0;
       if (do_qk || do_pv) tc_fence_after();
       if (do_pv) {
         if (leader) {
@@ -715,18 +721,23 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
       }
       if (do_qk) {
         if (leader) {
-          const int h0 = lat_half<SM::kHalves>(2 * i).slot, h1 = lat_half<SM::kHalves>(2 * i + 1).slot;
-          const uint64_t rot = static_cast<uint64_t>(i % SM::kRots * kLatRot) >> 4;
           const uint32_t d = tmem + SM::kTmemS + buf * SM::kQRows;
+          const uint64_t rows = desc_k + h.slot * (kLatHalf >> 4);
+          if (half == 0) {
+            const uint64_t rot = desc_rot + (static_cast<uint64_t>(i % SM::kRots * kLatRot) >> 4);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            umma_f8(d, desc_rot + rot + k * 2, desc_q + (32 + k * 2) * SM::kQRows, kIdescS, k > 0 ? 1u : 0u);
+            for (int k = 0; k < 2; ++k)
+              umma_f8(d, rot + k * 2, desc_q + (32 + k * 2) * SM::kQRows, kIdescS, k > 0 ? 1u : 0u);
+            umma_commit(&s->rot_empty[i % SM::kRots]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int k = 0; k < 8; ++k)
+              umma_f8(d, rows + (k >> 2) * (kLatChunk >> 4) + (k & 3) * 2, desc_q + k * 2 * SM::kQRows, kIdescS, 1u);
+          } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8(d, desc_k + (c < 2 ? h0 : h1) * (kLatHalf >> 4) + (c & 1) * (kLatChunk >> 4) + k * 2, desc_q + (c * 8 + k * 2) * SM::kQRows, kIdescS, 1u);
-          umma_commit(&s->s_full[buf]);
+            for (int k = 0; k < 8; ++k)
+              umma_f8(d, rows + (k >> 2) * (kLatChunk >> 4) + (k & 3) * 2, desc_q + (16 + k * 2) * SM::kQRows, kIdescS, 1u);
+            umma_commit(&s->s_full[buf]);
+          }
         }
         __syncwarp();
         ++qk;
@@ -747,6 +758,7 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
 template <int HG, bool SMALL>
 __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename LatSmem<HG>::Info* s,
                                                LatSchedule<HG>& schedule) {
+  using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
   const int lane = threadIdx.x & 31;
   const int ps = a.table.page_size, run = a.run;
@@ -790,7 +802,7 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
       *reinterpret_cast<float4*>(&s->scale[slot][4 * lane]) = make_float4(sc[0], sc[1], sc[2], sc[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->scale_full[slot]);
-      if (++slot == kLatAhead) { slot = 0; phase ^= 1u; }
+      if (++slot == SM::kAhead) { slot = 0; phase ^= 1u; }
     }
     if (!f.valid) return true;
   }
@@ -809,8 +821,8 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
   const bool leader = elect_one();
   const int run = a.run, pieces = kLatTile / run;
   for (int it = 0;; ++it) {
-    const int ahead = it % kLatAhead;
-    if (!__all_sync(0xffffffffu, lat_wait(&s->rows_full[ahead], (it / kLatAhead) & 1, abort_flag))) return false;
+    const int ahead = it % SM::kAhead;
+    if (!__all_sync(0xffffffffu, lat_wait(&s->rows_full[ahead], (it / SM::kAhead) & 1, abort_flag))) return false;
     const int live = __shfl_sync(0xffffffffu, s->live[ahead], 0);
     if (live < 0) return true;
     const int mine = s->rows[ahead][lane];
@@ -820,7 +832,9 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
     uint64_t* full = &s->kv_full[h.slot];
     uint8_t* dst = smem + h.slot * kLatHalf;
     uint8_t* rot = smem + SM::kOffRot + it % SM::kRots * kLatRot;
-    if (!__all_sync(0xffffffffu, lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag))) return false;
+    bool ok = lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag);
+    if (half == 0) ok = ok && lat_wait(&s->rot_empty[it % SM::kRots], ((it / SM::kRots) & 1) ^ 1u, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
     if (leader) mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
 #pragma unroll 1
     for (int i = 0, at = 0; i < pieces; ++i, at += run) {
@@ -866,8 +880,8 @@ __device__ __forceinline__ bool lat_copy_role(const LatAttnArgs& a, const uint8_
   };
   bool ok = true;
   for (int it = 0; ok; ++it) {
-    const int ahead = it % kLatAhead;
-    ok = wait(&s->rows_full[ahead], (it / kLatAhead) & 1);
+    const int ahead = it % SM::kAhead;
+    ok = wait(&s->rows_full[ahead], (it / SM::kAhead) & 1);
     if (!ok || s->live[ahead] < 0) break;
     const uint8_t* src[4];
 #pragma unroll
@@ -880,7 +894,8 @@ __device__ __forceinline__ bool lat_copy_role(const LatAttnArgs& a, const uint8_
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
-      ok = wait(&s->kv_empty[h.slot], h.phase ^ 1u);
+      ok = wait(&s->kv_empty[h.slot], h.phase ^ 1u) &&
+           (half == 1 || wait(&s->rot_empty[it % SM::kRots], ((it / SM::kRots) & 1) ^ 1u));
       if (!ok) break;
       const uint32_t dst = in_tile + h.slot * kLatHalf, rot = in_rot + it % SM::kRots * kLatRot;
 #pragma unroll
@@ -920,8 +935,20 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   volatile int* abort_flag = &s->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kGroups = SM::kGroups;
+  if (smem + SM::kUsed > smem_raw + SM::kBytes) {          // (an unaligned start of shared memory)
+    if (threadIdx.x == 0) {
+      raise_device_error(FP8MOE_DEVERR_TIMEOUT);
+      a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < SM::kRots; ++i) mbar_init(&s->rot_empty[i], 1);
+    for (int i = 0; i < SM::kPBufs; ++i) {
+      mbar_init(&s->p_full[i], 4 * kGroups);
+      mbar_init(&s->p_empty[i], 1);
+    }
     for (int i = 0; i < SM::kHalves; ++i) {
       mbar_init(&s->kv_full[i], SMALL ? 4 : 1);
       mbar_init(&s->kv_empty[i], 1);
@@ -929,13 +956,11 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->s_empty[i], 4 * kGroups);
-      mbar_init(&s->p_full[i], 4 * kGroups);
-      mbar_init(&s->p_empty[i], 1);
       mbar_init(&s->frag_full[i], 1);
       mbar_init(&s->frag_empty[i], 1 + 4 * kGroups);
     }
     for (int g = 0; g < kGroups; ++g) s->flag[g][0] = s->flag[g][1] = s->flag[g][2] = 0;
-    for (int i = 0; i < kLatAhead; ++i) {
+    for (int i = 0; i < SM::kAhead; ++i) {
       mbar_init(&s->rows_full[i], 1);
       mbar_init(&s->scale_full[i], 1);
       mbar_init(&s->tab_empty[i], (SMALL ? 4 : 2) + 4 * kGroups);
