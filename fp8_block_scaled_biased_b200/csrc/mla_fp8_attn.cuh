@@ -145,6 +145,14 @@ __device__ __forceinline__ LatHalf lat_half(int n) {
 }
 
 // ---------------------------------------------------------------- PTX
+// tma_load_2d on shared-memory addresses computed once.
+__device__ __forceinline__ void tma_load_at(uint32_t smem_dst, uint64_t map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
 __device__ __forceinline__ void cp_async_16(uint32_t smem_dst, const void* gmem_src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gmem_src) : "memory");
 }
@@ -699,26 +707,7 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
       const bool do_qk = qk < 2 * n && qk <= 2 * pv + 3 && (ready & 3u) == 3u;
       const bool do_pv = 2 * pv + 2 <= qk && (ready & 4u) != 0;
       if (do_qk || do_pv) tc_fence_after();
-      if (do_pv) {
-        if (leader) {
-          const int h0 = lat_half<SM::kHalves>(2 * j).slot, h1 = lat_half<SM::kHalves>(2 * j + 1).slot;
-          const uint64_t p = desc_p + (pbuf * (SM::kPBytes >> 4));
-          const uint32_t more = pv > 0 ? 1u : 0u;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8(tmem + SM::kTmemO + m * SM::kPRows,
-                      desc_v + (m < 2 ? h0 : h1) * (kLatHalf >> 4) + (m & 1) * (kLatChunk >> 4) + k * 256, p + k * 32,
-                      kIdescO, k > 0 ? 1u : more);
-            if (m & 1) umma_commit(&s->kv_empty[m < 2 ? h0 : h1]);
-          }
-          umma_commit(&s->p_empty[pbuf]);
-        }
-        __syncwarp();
-        ++pv;
-        spin = 0;
-      }
+      // scores first: the softmax warps wait for them, and a half takes the MMAs half as long as P V
       if (do_qk) {
         if (leader) {
           const uint32_t d = tmem + SM::kTmemS + buf * SM::kQRows;
@@ -741,6 +730,26 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
         }
         __syncwarp();
         ++qk;
+        spin = 0;
+      }
+      if (do_pv) {
+        if (leader) {
+          const int h0 = lat_half<SM::kHalves>(2 * j).slot, h1 = lat_half<SM::kHalves>(2 * j + 1).slot;
+          const uint64_t p = desc_p + (pbuf * (SM::kPBytes >> 4));
+          const uint32_t more = pv > 0 ? 1u : 0u;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_f8(tmem + SM::kTmemO + m * SM::kPRows,
+                      desc_v + (m < 2 ? h0 : h1) * (kLatHalf >> 4) + (m & 1) * (kLatChunk >> 4) + k * 256, p + k * 32,
+                      kIdescO, k > 0 ? 1u : more);
+            if (m & 1) umma_commit(&s->kv_empty[m < 2 ? h0 : h1]);
+          }
+          umma_commit(&s->p_empty[pbuf]);
+        }
+        __syncwarp();
+        ++pv;
         spin = 0;
       }
       if (spin == 64) t0 = global_timer_ns();
@@ -812,14 +821,17 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
 // rotary entries and chunks 0, 1; half 1: chunks 2, 3) as P V frees them. As in the MMA warp all lanes
 // run the loop and one issues: a copy takes 80 cycles to issue beside the softmax warps, 100 to 150
 // from a divergent branch.
-template <int HG>
+template <int HG, int half>
 __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtensorMap* tm_lat, const CUtensorMap* tm_rot,
-                                              typename LatSmem<HG>::Info* s, uint8_t* smem, int half) {
+                                              typename LatSmem<HG>::Info* s, uint8_t* smem) {
   using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   const int run = a.run, pieces = kLatTile / run;
+  const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+  const uint32_t bars = __shfl_sync(0xffffffffu, smem_u32(&s->kv_full[0]), 0);
+  const uint64_t lat = reinterpret_cast<uint64_t>(tm_lat), rotary = reinterpret_cast<uint64_t>(tm_rot);
   for (int it = 0;; ++it) {
     const int ahead = it % SM::kAhead;
     if (!__all_sync(0xffffffffu, lat_wait(&s->rows_full[ahead], (it / SM::kAhead) & 1, abort_flag))) return false;
@@ -829,21 +841,22 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
     __syncwarp();
     if (leader) mbar_arrive(&s->tab_empty[ahead]);
     const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
-    uint64_t* full = &s->kv_full[h.slot];
-    uint8_t* dst = smem + h.slot * kLatHalf;
-    uint8_t* rot = smem + SM::kOffRot + it % SM::kRots * kLatRot;
     bool ok = lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag);
     if (half == 0) ok = ok && lat_wait(&s->rot_empty[it % SM::kRots], ((it / SM::kRots) & 1) ^ 1u, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
-    if (leader) mbar_arrive_expect_tx(full, live * (half == 0 ? 320 : 256));
-#pragma unroll 1
-    for (int i = 0, at = 0; i < pieces; ++i, at += run) {
+    const uint32_t full = bars + h.slot * 8;
+    uint32_t dst = base + h.slot * kLatHalf, rot = base + SM::kOffRot + it % SM::kRots * kLatRot;
+    if (leader) mbar_arrive_expect_tx(&s->kv_full[h.slot], live * (half == 0 ? 320 : 256));
+#pragma unroll 2
+    for (int i = 0; i < pieces; ++i) {
       const int row = __shfl_sync(0xffffffffu, mine, i);
       if (row >= 0 && leader) {
-        if (half == 0) tma_load_2d(rot + at * 64, tm_rot, full, 512, row);
-        tma_load_2d(dst + at * 128, tm_lat, full, half * 256, row);
-        tma_load_2d(dst + kLatChunk + at * 128, tm_lat, full, half * 256 + 128, row);
+        tma_load_at(dst, lat, full, half * 256, row);
+        tma_load_at(dst + kLatChunk, lat, full, half * 256 + 128, row);
+        if (half == 0) tma_load_at(rot, rotary, full, 512, row);
       }
+      dst += run * 128;
+      rot += run * 64;
     }
     __syncwarp();
   }
@@ -1037,7 +1050,7 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     ok = lat_table_role<HG, SMALL>(a, s, schedule);
     if (!ok && lane == 0) a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);   // the joining kernel must not find old words
   } else if constexpr (!SMALL) {
-    ok = lat_load_role<HG>(a, &tm_lat, &tm_rot, s, smem, warp >> 1);
+    ok = warp == 0 ? lat_load_role<HG, 0>(a, &tm_lat, &tm_rot, s, smem) : lat_load_role<HG, 1>(a, &tm_lat, &tm_rot, s, smem);
     if (!ok) {
       // copies already in flight must land before the CTA's shared memory goes away
       const unsigned long long t0 = global_timer_ns();
