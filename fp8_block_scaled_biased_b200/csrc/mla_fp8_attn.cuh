@@ -116,7 +116,6 @@ struct LatSmem {
     uint64_t kv_full[kHalves], kv_empty[kHalves], rot_empty[kRots];
     uint64_t s_full[2], s_empty[2], p_full[kPBufs], p_empty[kPBufs];
     uint64_t frag_full[2], frag_empty[2], q_full;
-    int flag[kGroups][3];         // a score passed its reference's bound (1), a wait failed (2); tiles take turns
     long long scan[24];
     long long start_off;          // position of the first sequence of this CTA's share,
     int start_b;                  // the sequence, and its shape
@@ -331,15 +330,36 @@ struct LatSchedule {
 };
 
 // ---------------------------------------------------------------- softmax warpgroup
-// Codes of two columns (two bytes) of the three terms of y in [0, 2^8]: y is rounded to the 11 bits
-// of fp16, of which hi takes 4, lo 4 and lo2 the rest, exactly (down to lo2's subnormals).
-__device__ __forceinline__ void split_weights(float y0, float y1, uint16_t& hi, uint16_t& lo, uint16_t& lo2) {
-  const __half2 k32 = __float2half2_rn(32.0f);
-  const __half2 y = __floats2half2_rn(y0, y1);
-  hi = half2_to_e4m3x2(y);
-  const __half2 r = __hmul2(__hsub2(y, e4m3x2_to_half2(hi)), k32);     // at most half a step of hi: 8 * 32
-  lo = half2_to_e4m3x2(r);
-  lo2 = half2_to_e4m3x2(__hmul2(__hsub2(r, e4m3x2_to_half2(lo)), k32));
+// Four values as four codes per term; halves of words are handled as such, without 16-bit arithmetic.
+// Weights in [0, 2^8]: rounded to the 11 bits of fp16, of which hi takes 4, lo 4 and lo2 the rest,
+// exactly (down to lo2's subnormals): y = hi + lo / 32 + lo2 / 1024. The rest after a term is at most
+// half its last step, so 32 times that fits the next.
+__device__ __forceinline__ void split_weights(float y0, float y1, float y2, float y3, uint32_t& hi, uint32_t& lo,
+                                              uint32_t& lo2) {
+  asm("{\n\t.reg .b32 a, b, x, y, k;\n\t.reg .b16 p, q;\n\t"
+      "mov.b32 k, 0x50005000;\n\t"                          // 32, 32
+      "cvt.rn.f16x2.f32 a, %4, %3;\n\tcvt.rn.f16x2.f32 b, %6, %5;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, a;\n\tcvt.rn.satfinite.e4m3x2.f16x2 q, b;\n\tmov.b32 %0, {p, q};\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, p;\n\tcvt.rn.f16x2.e4m3x2 y, q;\n\t"
+      "sub.rn.f16x2 a, a, x;\n\tsub.rn.f16x2 b, b, y;\n\tmul.rn.f16x2 a, a, k;\n\tmul.rn.f16x2 b, b, k;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, a;\n\tcvt.rn.satfinite.e4m3x2.f16x2 q, b;\n\tmov.b32 %1, {p, q};\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, p;\n\tcvt.rn.f16x2.e4m3x2 y, q;\n\t"
+      "sub.rn.f16x2 a, a, x;\n\tsub.rn.f16x2 b, b, y;\n\tmul.rn.f16x2 a, a, k;\n\tmul.rn.f16x2 b, b, k;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, a;\n\tcvt.rn.satfinite.e4m3x2.f16x2 q, b;\n\tmov.b32 %2, {p, q};\n\t}"
+      : "=r"(hi), "=r"(lo), "=r"(lo2)
+      : "f"(y0), "f"(y1), "f"(y2), "f"(y3));
+}
+// Query entries of at most 448 in magnitude: x = hi + lo / 16.
+__device__ __forceinline__ void split_query(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b32 a, b, x, y, k;\n\t.reg .b16 p, q;\n\t"
+      "mov.b32 k, 0x4c004c00;\n\t"                          // 16, 16
+      "cvt.rn.f16x2.f32 a, %3, %2;\n\tcvt.rn.f16x2.f32 b, %5, %4;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, a;\n\tcvt.rn.satfinite.e4m3x2.f16x2 q, b;\n\tmov.b32 %0, {p, q};\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, p;\n\tcvt.rn.f16x2.e4m3x2 y, q;\n\t"
+      "sub.rn.f16x2 a, a, x;\n\tsub.rn.f16x2 b, b, y;\n\tmul.rn.f16x2 a, a, k;\n\tmul.rn.f16x2 b, b, k;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, a;\n\tcvt.rn.satfinite.e4m3x2.f16x2 q, b;\n\tmov.b32 %1, {p, q};\n\t}"
+      : "=r"(hi), "=r"(lo)
+      : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
 }
 
 __device__ __forceinline__ int float_order(float x) {      // order of floats as order of ints
@@ -384,17 +404,14 @@ struct LatQueries {
     for (int d = 1; d < 16; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     const int ex = max(kScaleMinExp, static_cast<int>(mx >> 7) - 135 + ((mx & 0x7fu) > 96u ? 1 : 0));
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-    const __half2 k16 = __float2half2_rn(16.0f);
     uint8_t* dst = qs + ((tid & 15) >> 2) * kLead + (tid & 3) * 4 + (group * 16 + (tid >> 4)) * 16;
 #pragma unroll
     for (int j = 0; j < 9; ++j, dst += 4 * kLead) {        // 64 entries on
       const float2 v0 = bf16x2_to_float(x[j].x), v1 = bf16x2_to_float(x[j].y);
-      const __half2 h0 = __floats2half2_rn(v0.x * inv, v0.y * inv), h1 = __floats2half2_rn(v1.x * inv, v1.y * inv);
-      const uint16_t hi0 = half2_to_e4m3x2(h0), hi1 = half2_to_e4m3x2(h1);         // at most 448: h exact above 2^-16
-      const uint16_t lo0 = half2_to_e4m3x2(__hmul2(__hsub2(h0, e4m3x2_to_half2(hi0)), k16));
-      const uint16_t lo1 = half2_to_e4m3x2(__hmul2(__hsub2(h1, e4m3x2_to_half2(hi1)), k16));
-      *reinterpret_cast<uint32_t*>(dst) = hi0 | (static_cast<uint32_t>(hi1) << 16);
-      *reinterpret_cast<uint32_t*>(dst + 128) = lo0 | (static_cast<uint32_t>(lo1) << 16);
+      uint32_t hi, lo;                                     // (x / scale is exact in fp16 above 2^-16)
+      split_query(v0.x * inv, v0.y * inv, v1.x * inv, v1.y * inv, hi, lo);
+      *reinterpret_cast<uint32_t*>(dst) = hi;
+      *reinterpret_cast<uint32_t*>(dst + 128) = lo;
     }
     return mx >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
   }
@@ -417,11 +434,9 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
   const bool capped = a.logit_cap > 0.0f;
   // cap * tanh(t / cap) * log2(e) = cap2 - 2 cap2 / (1 + 2^(t cap_in)): off by a few 2^-24 of the cap
   const float cap2 = a.logit_cap * kLog2e, cap_in = 2.0f * kLog2e / a.logit_cap;
-  volatile int* flag = &s->flag[group][0];
   int fslot = 0;
   uint32_t fphase = 0;
   int it = 0;                                              // tiles so far: buffers and phases follow it
-  int turn = 0;                                            // it % 3
   int nfrag = 0;
   LatFragment f;
   bool ok;
@@ -459,7 +474,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     const int sees_min = f.sees0 + query;                  // of this group's first column
     const int next_query = (query + 1) * a.Hq - (f.col0 + group * 8);  // columns until the next query
 
-    for (int tile = f.tile0; tile < f.tile1; ++tile, ++it, turn = turn == 2 ? 0 : turn + 1) {
+    for (int tile = f.tile0; tile < f.tile1; ++tile, ++it) {
       const int buf = it & 1, pbuf = it % SM::kPBufs;
       const uint32_t phase = (it >> 1) & 1;
       const int ahead = it % SM::kAhead;
@@ -471,16 +486,16 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       const float bound = kLatTopExp - (sc > 0.0f ? __log2f(sc) : -100.0f);
       float2 fs[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fs[i] = make_float2(fac[2 * i] * sc, fac[2 * i + 1] * sc);
+      for (int i = 0; i < 4; ++i) fs[i] = __fmul2_rn(make_float2(fac[2 * i], fac[2 * i + 1]), make_float2(sc, sc));
+      if (SM::kPBufs == 2) ok = lat_wait(&s->p_empty[pbuf], ((it / SM::kPBufs) & 1) ^ 1u, abort_flag) && ok;
       ok = lat_wait(&s->s_full[buf], phase, abort_flag) && ok;
-      ok = __all_sync(0xffffffffu, ok);
+      __syncwarp();
       tc_fence_after();
       float t[8];
       {
         float v[16];
         tmem_load_16(lane_base + SM::kTmemS + buf * SM::kQRows + group * 16, v);
         tc_fence_before();
-        if (lane == 0) mbar_arrive(&s->s_empty[buf]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 x = __fmul2_rn(__ffma2_rn(make_float2(v[8 + 2 * i], v[9 + 2 * i]), make_float2(0.0625f, 0.0625f),
@@ -509,18 +524,18 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
           if (--left == 0) { left = a.Hq; ++sees; }
         }
       }
-      // A score that passes its bound raises a flag, which is read after the barrier below; until then
-      // the weights are computed as if there were none. A fragment's first tile has no references yet:
-      // it takes them first. (fmaxf passes over NaN.)
+      // The weights are computed before the group has agreed, in a barrier, that no score passes its
+      // bound; if one does, the references move and they are computed again. A fragment's first tile has
+      // no references yet: it takes them first. (fmaxf passes over NaN.)
       bool moves = tile == f.tile0;
       float w[8], top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        w[c] = t[c] + nref[c];
-        top = fmaxf(top, w[c]);
+      for (int c = 0; c < 8; c += 2) {
+        const float2 x = __fadd2_rn(make_float2(t[c], t[c + 1]), make_float2(nref[c], nref[c + 1]));
+        w[c] = x.x;
+        w[c + 1] = x.y;
+        top = fmaxf(top, fmaxf(x.x, x.y));
       }
-      if (!moves && top > bound) atomicOr(const_cast<int*>(&flag[turn]), 1);
-      if (!ok) atomicOr(const_cast<int*>(&flag[turn]), 2);
       uint32_t hi[2], lo[2], lo2[2];
       for (;;) {
         if (moves) {
@@ -532,7 +547,12 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
             const int m = __reduce_max_sync(0xffffffffu, float_order(x));
             if (lane == 0) s->red[group][warp][c] = order_float(m);
           }
-          ok = (tile == f.tile0 || lat_wait(&s->p_empty[(it - 1) % SM::kPBufs], ((it - 1) / SM::kPBufs) & 1, abort_flag)) && ok;
+          if (tile == f.tile0) {
+            if (lane == 0) mbar_arrive(&s->s_empty[buf]);
+            if (SM::kPBufs == 1) ok = lat_wait(&s->p_empty[pbuf], ((it / SM::kPBufs) & 1) ^ 1u, abort_flag) && ok;
+          } else {
+            ok = lat_wait(&s->p_empty[(it - 1) % SM::kPBufs], ((it - 1) / SM::kPBufs) & 1, abort_flag) && ok;
+          }
           if (group_any(bar_id, !ok)) return false;
           float alpha[8];
 #pragma unroll
@@ -545,6 +565,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
             sum[c] *= alpha[c];
             w[c] = t[c] + next;
           }
+          group_sync(bar_id);                              // red may be written again
           if (tile > f.tile0) {                            // what has been summed, in the new references
             tc_fence_after();
 #pragma unroll 1
@@ -563,24 +584,18 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
         for (int c = 0; c < 8; ++c) w[c] = exp2_fast(w[c]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint16_t h[2], l[2], l2[2];
-          split_weights(w[4 * i] * sc, w[4 * i + 1] * sc, h[0], l[0], l2[0]);
-          split_weights(w[4 * i + 2] * sc, w[4 * i + 3] * sc, h[1], l[1], l2[1]);
-          hi[i] = h[0] | (static_cast<uint32_t>(h[1]) << 16);
-          lo[i] = l[0] | (static_cast<uint32_t>(l[1]) << 16);
-          lo2[i] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
+          const float2 y0 = __fmul2_rn(make_float2(w[4 * i], w[4 * i + 1]), make_float2(sc, sc));
+          const float2 y1 = __fmul2_rn(make_float2(w[4 * i + 2], w[4 * i + 3]), make_float2(sc, sc));
+          split_weights(y0.x, y0.y, y1.x, y1.y, hi[i], lo[i], lo2[i]);
         }
+        if (moves) break;
+        if (lane == 0) mbar_arrive(&s->s_empty[buf]);
         // the P V that read this buffer before is done
-        ok = lat_wait(&s->p_empty[pbuf], ((it / SM::kPBufs) & 1) ^ 1u, abort_flag);
-        if (!ok) atomicOr(const_cast<int*>(&flag[turn]), 2);
-        group_sync(bar_id);                                // (red, too, may be written again after it)
-        const int raised = flag[turn];
-        if (raised & 2) return false;
-        if (moves || !raised) break;
+        if (SM::kPBufs == 1) ok = lat_wait(&s->p_empty[pbuf], ((it / SM::kPBufs) & 1) ^ 1u, abort_flag) && ok;
+        if (!group_any(bar_id, top > bound || !ok)) break;
+        if (group_any(bar_id, !ok)) return false;
         moves = true;
       }
-      // the flag of the tile after the next: read before this barrier, raised after the next one
-      if (tid == 0) flag[turn == 0 ? 2 : turn - 1] = 0;
       uint8_t* pb = smem + SM::kOffP + pbuf * SM::kPBytes + tid * 16;
       *reinterpret_cast<uint4*>(pb + block * (16 * kLatTile)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
       *reinterpret_cast<uint2*>(pb + block2 * (16 * kLatTile) + half8) = make_uint2(lo2[0], lo2[1]);
@@ -596,7 +611,11 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->p_full[pbuf]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] += w[c];
+      for (int c = 0; c < 8; c += 2) {
+        const float2 x = __fadd2_rn(make_float2(sum[c], sum[c + 1]), make_float2(w[c], w[c + 1]));
+        sum[c] = x.x;
+        sum[c + 1] = x.y;
+      }
     }
 
     // ---- the next fragment's queries, so that its first scores are on their way; then this one's result:
@@ -635,15 +654,25 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     if (f.slot < 0) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum[c] = s->inv[group][c];
-      __nv_bfloat16* dst = a.o + row0 * kLatDv + tid;
-#pragma unroll 1
-      for (int m = 0; m < 4; ++m, dst += 128) {
+      // neighbouring lanes share the work: the even one stores both values of columns 0 .. 3, the odd one
+      // those of 4 .. 7 (half as many, twice as wide stores)
+      const bool odd = lane & 1;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (row0 + (odd ? 4 : 0)) * kLatDv) + (tid >> 1);
+      const int mine = live - (odd ? 4 : 0);
+#pragma unroll 2
+      for (int m = 0; m < 4; ++m, dst += 64) {
         float x[24];
         tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float y = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]) * sum[c];
-          if (c < live) dst[c * kLatDv] = __float2bfloat16(sum[c] == 0.0f ? 0.0f : y);
+          x[c] = sum[c] == 0.0f ? 0.0f : y;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float other = __shfl_xor_sync(0xffffffffu, odd ? x[c] : x[4 + c], 1);
+          const __nv_bfloat162 y = odd ? __floats2bfloat162_rn(other, x[4 + c]) : __floats2bfloat162_rn(x[c], other);
+          if (c < mine) dst[c * (kLatDv / 2)] = *reinterpret_cast<const uint32_t*>(&y);
         }
       }
     } else {                                               // a part, as it stands
@@ -972,7 +1001,6 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
       mbar_init(&s->frag_full[i], 1);
       mbar_init(&s->frag_empty[i], 1 + 4 * kGroups);
     }
-    for (int g = 0; g < kGroups; ++g) s->flag[g][0] = s->flag[g][1] = s->flag[g][2] = 0;
     for (int i = 0; i < SM::kAhead; ++i) {
       mbar_init(&s->rows_full[i], 1);
       mbar_init(&s->scale_full[i], 1);
