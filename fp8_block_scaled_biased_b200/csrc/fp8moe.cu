@@ -1245,6 +1245,8 @@ static int lat_launch(const char* name, LatAttnArgs a, const CUtensorMap& lat, c
   a.part_o = reinterpret_cast<float*>(ws + lat_acc_offset(HG));
   mla_fp8_kernel<HG, SMALL><<<ctas, kLatThreads<HG, SMALL>, LatSmem<HG>::kBytes, st>>>(lat, rot, a);
   if (int rc = check_launch(name)) return rc;
+  // a table of one tile cuts nothing
+  if (static_cast<long long>(a.table.num_indices) * a.table.page_size <= kLatTile) return FP8MOE_OK;
   // launched while the attention kernel runs (programmatic dependence): it waits for its end itself
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas, HG / 2);

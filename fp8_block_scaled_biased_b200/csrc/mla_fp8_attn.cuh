@@ -460,9 +460,84 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     if (tid == 0) mbar_arrive(&s->q_full);
     return true;
   };
-  if (!next_fragment(f)) return false;
-  while (f.valid) {
-    float fac[8], nref[8], sum[8];                         // nref: code exponent of the reference minus the reference
+  float nref[8], sum[8];         // of each column: code exponent of the reference minus the reference; sum of weights
+  f.valid = 0;
+  for (;;) {
+    // the next fragment's queries first, so that its scores are on their way while this one's result (the
+    // columns' sums over all threads, the accumulators) is written
+    LatFragment next;
+    if (!next_fragment(next)) return false;
+    if (f.valid) {
+      ok = lat_wait(&s->p_empty[(it - 1) % SM::kPBufs], ((it - 1) / SM::kPBufs) & 1, abort_flag);
+      // lane bits 4 .. 2 choose a half of the columns each: four lanes end with parts of one column's sum
+#pragma unroll
+      for (int h = 4; h; h >>= 1) {
+        const bool upper = (lane & (4 * h)) != 0;
+#pragma unroll
+        for (int c = 0; c < h; ++c) {
+          const float keep = upper ? sum[c + h] : sum[c], give = upper ? sum[c] : sum[c + h];
+          sum[c] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * h);
+        }
+      }
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+      if ((lane & 3) == 0) s->red[group][warp][lane >> 2] = sum[0];
+      if (group_any(bar_id, !ok)) return false;
+      tc_fence_after();
+      const int live = min(8, f.cols - group * 8);
+      const size_t row0 = static_cast<size_t>(f.row0) + group * 8;
+      const size_t part0 = static_cast<size_t>(max(f.slot, 0)) * HG + group * 8;
+      if (tid < 8) {
+        const float l = (s->red[group][0][tid] + s->red[group][1][tid]) + (s->red[group][2][tid] + s->red[group][3][tid]);
+        const float m = pick8(nref, tid);                    // l sums 2^(score + m)
+        if (tid < live) {
+          if (f.slot >= 0) a.part_ml[part0 + tid] = make_float2(m, l);
+          else if (a.lse) a.lse[row0 + tid] = l == 0.0f ? -INFINITY : (log2f(l) - m) * kLn2;
+        }
+        s->inv[group][tid] = l == 0.0f ? 0.0f : 1.0f / l;
+      }
+      group_sync(bar_id);
+      if (f.slot < 0) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sum[c] = s->inv[group][c];
+        // neighbouring lanes share the work: the even one stores both values of columns 0 .. 3, the odd one
+        // those of 4 .. 7 (half as many, twice as wide stores)
+        const bool odd = lane & 1;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (row0 + (odd ? 4 : 0)) * kLatDv) + (tid >> 1);
+        const int mine = live - (odd ? 4 : 0);
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m, dst += 64) {
+          float x[24];
+          tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float y = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]) * sum[c];
+            x[c] = sum[c] == 0.0f ? 0.0f : y;
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? x[c] : x[4 + c], 1);
+            const __nv_bfloat162 y = odd ? __floats2bfloat162_rn(other, x[4 + c]) : __floats2bfloat162_rn(x[c], other);
+            if (c < mine) dst[c * (kLatDv / 2)] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+        }
+      } else {                                               // a part, as it stands
+        float* dst = a.part_o + part0 * kLatDv + tid;
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m, dst += 128) {
+          float x[24];
+          tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < live) dst[c * kLatDv] = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]);
+        }
+      }
+      tc_fence_before();
+      group_sync(bar_id);                                    // red, inv and TMEM are read before what comes next
+    }
+    if (!next.valid) return true;
+    f = next;
+    float fac[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       fac[c] = s->qfac[(nfrag - 1) & 1][group][c];
@@ -618,79 +693,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       }
     }
 
-    // ---- the next fragment's queries, so that its first scores are on their way; then this one's result:
-    // the columns' sums over all threads, and the accumulators
-    LatFragment next;
-    if (!next_fragment(next)) return false;
-    ok = lat_wait(&s->p_empty[(it - 1) % SM::kPBufs], ((it - 1) / SM::kPBufs) & 1, abort_flag);
-    // lane bits 4 .. 2 choose a half of the columns each: four lanes end with parts of one column's sum
-#pragma unroll
-    for (int h = 4; h; h >>= 1) {
-      const bool upper = (lane & (4 * h)) != 0;
-#pragma unroll
-      for (int c = 0; c < h; ++c) {
-        const float keep = upper ? sum[c + h] : sum[c], give = upper ? sum[c] : sum[c + h];
-        sum[c] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * h);
-      }
-    }
-    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
-    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-    if ((lane & 3) == 0) s->red[group][warp][lane >> 2] = sum[0];
-    if (group_any(bar_id, !ok)) return false;
-    tc_fence_after();
-    const int live = min(8, f.cols - group * 8);
-    const size_t row0 = static_cast<size_t>(f.row0) + group * 8;
-    const size_t part0 = static_cast<size_t>(max(f.slot, 0)) * HG + group * 8;
-    if (tid < 8) {
-      const float l = (s->red[group][0][tid] + s->red[group][1][tid]) + (s->red[group][2][tid] + s->red[group][3][tid]);
-      const float m = pick8(nref, tid);                    // l sums 2^(score + m)
-      if (tid < live) {
-        if (f.slot >= 0) a.part_ml[part0 + tid] = make_float2(m, l);
-        else if (a.lse) a.lse[row0 + tid] = l == 0.0f ? -INFINITY : (log2f(l) - m) * kLn2;
-      }
-      s->inv[group][tid] = l == 0.0f ? 0.0f : 1.0f / l;
-    }
-    group_sync(bar_id);
-    if (f.slot < 0) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] = s->inv[group][c];
-      // neighbouring lanes share the work: the even one stores both values of columns 0 .. 3, the odd one
-      // those of 4 .. 7 (half as many, twice as wide stores)
-      const bool odd = lane & 1;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (row0 + (odd ? 4 : 0)) * kLatDv) + (tid >> 1);
-      const int mine = live - (odd ? 4 : 0);
-#pragma unroll 2
-      for (int m = 0; m < 4; ++m, dst += 64) {
-        float x[24];
-        tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float y = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]) * sum[c];
-          x[c] = sum[c] == 0.0f ? 0.0f : y;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float other = __shfl_xor_sync(0xffffffffu, odd ? x[c] : x[4 + c], 1);
-          const __nv_bfloat162 y = odd ? __floats2bfloat162_rn(other, x[4 + c]) : __floats2bfloat162_rn(x[c], other);
-          if (c < mine) dst[c * (kLatDv / 2)] = *reinterpret_cast<const uint32_t*>(&y);
-        }
-      }
-    } else {                                               // a part, as it stands
-      float* dst = a.part_o + part0 * kLatDv + tid;
-#pragma unroll 1
-      for (int m = 0; m < 4; ++m, dst += 128) {
-        float x[24];
-        tmem_load_16_8(acc1 + m * SM::kPRows, acc2 + m * SM::kPRows, x);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c < live) dst[c * kLatDv] = fmaf(fmaf(x[16 + c], 0.03125f, x[8 + c]), 0.03125f, x[c]);
-      }
-    }
-    tc_fence_before();
-    group_sync(bar_id);                                    // red, inv and TMEM are read before what comes next
-    f = next;
   }
-  return true;
 }
 
 // ---------------------------------------------------------------- MMA warp
