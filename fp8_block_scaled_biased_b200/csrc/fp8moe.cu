@@ -1249,8 +1249,8 @@ static int lat_launch(const char* name, LatAttnArgs a, const CUtensorMap& lat, c
   if (static_cast<long long>(a.table.num_indices) * a.table.page_size <= kLatTile) return FP8MOE_OK;
   // launched while the attention kernel runs (programmatic dependence): it waits for its end itself
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, HG / 2);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(ctas, HG);
+  cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1100,46 +1100,84 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   }
 }
 
-// Joins the parts of the column groups that were cut: half a block per (CTA that holds a first part,
-// column), four value columns per thread, eight parts' loads in flight; parts in order, so the same
-// bits every time. A part holds sums of 2^(score + m) and of those times values.
+// A weighted sum of parts under one reference (the largest is the least m), which moves as parts join.
+template <int N>
+struct LatSum {
+  float m = kLatNoRef, l = 0.0f;
+  float4 acc[N];
+  __device__ __forceinline__ LatSum() {
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  __device__ __forceinline__ void add(const float2 ml, const float4 (&x)[N]) {
+    if (ml.y == 0.0f) return;
+    const float next = fminf(m, ml.x), w0 = exp2f(next - m), w1 = exp2f(next - ml.x);
+    m = next;
+    l = l * w0 + ml.y * w1;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      acc[j].x = acc[j].x * w0 + x[j].x * w1;
+      acc[j].y = acc[j].y * w0 + x[j].y * w1;
+      acc[j].z = acc[j].z * w0 + x[j].z * w1;
+      acc[j].w = acc[j].w * w0 + x[j].w * w1;
+    }
+  }
+  // values 4 i .. 4 i + 3 (i = at, at + step, ..) of output row `row`
+  __device__ __forceinline__ void store(const LatAttnArgs& a, size_t row, int at, int step) const {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      __align__(8) const __nv_bfloat162 y[2] = {__floats2bfloat162_rn(acc[j].x * inv, acc[j].y * inv),
+                                                __floats2bfloat162_rn(acc[j].z * inv, acc[j].w * inv)};
+      reinterpret_cast<uint2*>(a.o + row * kLatDv)[at + j * step] = *reinterpret_cast<const uint2*>(y);
+    }
+    if (a.lse && at == 0) a.lse[row] = l == 0.0f ? -INFINITY : (log2f(l) - m) * 0.6931471805599453f;
+  }
+};
+
+// Joins the parts of the column groups that were cut, in order, so the same bits every time. A part
+// holds sums of 2^(score + m) and of those times values. blockIdx.x is the CTA that holds a first part.
+// Up to eight parts: a warp per column, four columns a block. More (long contexts of few sequences):
+// a block per column, eight parts' loads in flight; with a warp per column the 74 parts of two
+// 128K-token sequences took 35 us more. Bound by three dependent reads from L2.
 template <int HG>
-__global__ void __launch_bounds__(256) mla_fp8_join_kernel(const LatAttnArgs a) {
+__global__ void __launch_bounds__(128) mla_fp8_join_kernel(const LatAttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
-  const int cta = blockIdx.x, c = blockIdx.y * 2 + (threadIdx.x >> 7), col = threadIdx.x & 127;
+  const int cta = blockIdx.x;
   const int4 job = a.merge[cta];
+  const int c = job.z <= 8 ? blockIdx.y * 4 + (threadIdx.x >> 5) : blockIdx.y;
   if (c >= job.y) return;                                  // (no columns: nothing to join)
-  float m = kLatNoRef, l = 0.0f;                           // reference (the largest is the least m) and sum so far
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? job.w : 2 * (cta + (i << a.gang_log))) * HG; };
+  if (job.z <= 8) {
+    const int lane = threadIdx.x & 31;
+    LatSum<4> sum;
+#pragma unroll 2
+    for (int i = 0; i < job.z; ++i) {
+      const size_t at = slot(i) + c;
+      float4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[j * 32 + lane];
+      sum.add(a.part_ml[at], x);
+    }
+    sum.store(a, static_cast<size_t>(job.x) + c, lane, 32);
+    return;
+  }
+  LatSum<1> sum;
   constexpr int kBatch = 8;
   for (int i0 = 0; i0 < job.z; i0 += kBatch) {
     float2 ml[kBatch];
-    float4 x[kBatch];
+    float4 x[kBatch][1];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k;
-      const size_t at = static_cast<size_t>(i == 0 ? job.w : 2 * (cta + (i << a.gang_log))) * HG + c;
-      ml[k] = i < job.z ? a.part_ml[at] : make_float2(kLatNoRef, 0.0f);
-      x[k] = i < job.z ? reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[col] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const size_t at = slot(min(i0 + k, job.z - 1)) + c;
+      ml[k] = a.part_ml[at];
+      if (i0 + k >= job.z) ml[k].y = 0.0f;
+      x[k][0] = reinterpret_cast<const float4*>(a.part_o + at * kLatDv)[threadIdx.x];
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (ml[k].y == 0.0f) continue;
-      const float next = fminf(m, ml[k].x), w0 = exp2f(next - m), w1 = exp2f(next - ml[k].x);
-      m = next;
-      l = l * w0 + ml[k].y * w1;
-      acc.x = acc.x * w0 + x[k].x * w1;
-      acc.y = acc.y * w0 + x[k].y * w1;
-      acc.z = acc.z * w0 + x[k].z * w1;
-      acc.w = acc.w * w0 + x[k].w * w1;
-    }
+    for (int k = 0; k < kBatch; ++k) sum.add(ml[k], x[k]);
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const size_t row = static_cast<size_t>(job.x) + c;
-  __align__(8) __nv_bfloat162 y[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv),
-                                      __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
-  reinterpret_cast<uint2*>(a.o + row * kLatDv)[col] = *reinterpret_cast<const uint2*>(y);
-  if (a.lse && col == 0) a.lse[row] = l == 0.0f ? -INFINITY : (log2f(l) - m) * 0.6931471805599453f;
+  sum.store(a, static_cast<size_t>(job.x) + c, threadIdx.x, 128);
 }
 
 }  // namespace fp8moe
