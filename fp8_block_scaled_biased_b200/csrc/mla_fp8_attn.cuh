@@ -393,8 +393,8 @@ struct LatQueries {
 
   // Splits the entries into their two terms and stores them as the score MMAs' B operand: core
   // matrices of 8 rows x 16 bytes, this group's rows being its 8 high terms, then its 8 low ones.
-  // Returns the scale of column tid / 16: NaN for a row with an entry that is not finite, which makes
-  // all its scores NaN whatever its codes are.
+  // Returns the scale of column tid / 16. A row with an entry that is not finite gets codes of 0 and the
+  // scale NaN, which makes all its scores NaN: a NaN before the scale is a cached token's.
   __device__ __forceinline__ float store(uint8_t* qs, int group, int tid) const {
     constexpr int kLead = LatSmem<HG>::kQRows * 16;        // from 16 entries to the next
     uint32_t mx = 0;
@@ -410,6 +410,7 @@ struct LatQueries {
       const float2 v0 = bf16x2_to_float(x[j].x), v1 = bf16x2_to_float(x[j].y);
       uint32_t hi, lo;                                     // (x / scale is exact in fp16 above 2^-16)
       split_query(v0.x * inv, v0.y * inv, v1.x * inv, v1.y * inv, hi, lo);
+      if (mx >= 0x7f80u) hi = lo = 0u;
       *reinterpret_cast<uint32_t*>(dst) = hi;
       *reinterpret_cast<uint32_t*>(dst + 128) = lo;
     }
@@ -558,7 +559,8 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       __syncwarp();
       if (lane == 0) mbar_arrive(&s->tab_empty[ahead]);
       // the reference of a column bounds score + log2(page scale): the weights that meet the codes
-      const float bound = kLatTopExp - (sc > 0.0f ? __log2f(sc) : -100.0f);
+      // (below 2^-90 they are counted as of that scale, so that a sum of weights cannot leave fp32)
+      const float bound = kLatTopExp - fmaxf(__log2f(sc), -90.0f);
       float2 fs[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) fs[i] = __fmul2_rn(make_float2(fac[2 * i], fac[2 * i + 1]), make_float2(sc, sc));
@@ -567,10 +569,12 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
       __syncwarp();
       tc_fence_after();
       float t[8];
+      bool bad;                                            // a NaN in this token's row (queries have none)
       {
         float v[16];
         tmem_load_16(lane_base + SM::kTmemS + buf * SM::kQRows + group * 16, v);
         tc_fence_before();
+        bad = isnan(v[0]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 x = __fmul2_rn(__ffma2_rn(make_float2(v[8 + 2 * i], v[9 + 2 * i]), make_float2(0.0625f, 0.0625f),
@@ -579,12 +583,6 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
           t[2 * i] = x.x;
           t[2 * i + 1] = x.y;
         }
-      }
-      bool bad = false;                                    // a NaN in this token's row: every score is NaN
-      if (isnan(t[0])) {
-        bad = true;
-#pragma unroll
-        for (int c = 1; c < 8; ++c) bad = bad && isnan(t[c]);
       }
       if (capped) {
 #pragma unroll

@@ -310,6 +310,60 @@ def test_decode_nan_stays_with_its_sequence_and_head():
     assert ((o.cpu().double() - ref).abs()[fine] <= bound[fine]).all()
 
 
+@pytest.mark.parametrize("H, bad", [(8, 0), (5, 0), (16, 3), (24, 17)])
+def test_decode_nan_in_one_head_leaves_the_others(H, bad):
+    b = Batch([130, 300], 16, seed=13).device()
+    q = b.q(2, H)
+    clean = q.clone()
+    q[:, bad, 40] = math.nan
+    o, lse = _decode(b, q)
+    assert torch.isnan(o[:, bad]).all() and torch.isnan(lse[:, bad]).all()
+    o2, lse2 = _decode(b, clean)
+    keep = [h for h in range(H) if h != bad]
+    assert torch.equal(o[:, keep], o2[:, keep]) and torch.equal(lse[:, keep], lse2[:, keep])
+
+
+@pytest.mark.parametrize("H", [1, 8, 16, 32])
+def test_extend_a_nan_query_leaves_the_other_queries(H):
+    b = Batch([200, 40], 64, seed=14).device()
+    qo = _indptr([6, 3])
+    q = b.q(9, H)
+    clean = q.clone()
+    q[1], q[6] = math.nan, math.inf
+    o, lse = _extend(b, q, qo)
+    o2, lse2 = _extend(b, clean, qo)
+    bad, keep = [1, 6], [0, 2, 3, 4, 5, 7, 8]
+    assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+
+
+def test_decode_scales_at_the_ends_of_their_range():
+    """The smallest scale an append writes, under scores that rise after the first tile by just
+    less than what moves a reference: the weights' sum stays finite. Any output is a mean of
+    values, so it is off by at most twice the largest, 448 * 2^-110."""
+    b = Batch([1600], 64, seed=15, scale_exp=(-110, -110))
+    late = torch.arange(1600) >= 128
+    flat = b.codes.view(-1, 576)
+    at = b.indices[torch.arange(1600) // 64].long() * 64 + torch.arange(1600) % 64
+    flat[at, 575] = e4m3_encode(torch.where(late, 128.0, 0.0))
+    b.device()
+    q = torch.zeros(1, 16, 576)
+    q[:, :, 575] = 2.0 ** 103 * 5.75 * math.log(2.0)
+    q = q.to(torch.bfloat16)
+    ref, ref_lse, _, size = M8.decode(q, b.codes, b.scales, *b.table, sm_scale=1.0)
+    many = 160                                             # so many on the same pages that none is cut up
+    b.dt = (torch.arange(many + 1, dtype=torch.int32, device=DEV) * 25, b.dt[1].repeat(many), b.dt[2].repeat(many))
+    o, lse = _decode(b, q.expand(many, 16, 576).contiguous(), sm_scale=1.0)
+    dl = (lse.cpu().double() - ref_lse).abs()
+    assert (dl <= 2.0 ** -17 * (1 + size) + 2.0 ** -21 * (1 + ref_lse.abs())).all()
+    assert ((o.cpu().double() - ref).abs() <= 2 * 448 * 2.0 ** -110).all()
+    for e in (-88, 100):                                   # where the weights still have their full precision
+        b = Batch([300, 90], 16, seed=16, scale_exp=(e, e)).device()
+        q = b.q(2, 16)
+        o, lse = _decode(b, q, sm_scale=2.0 ** (-5 - e) / 24)
+        _check(b, q, torch.arange(3), o, lse, sm_scale=2.0 ** (-5 - e) / 24)
+
+
 # ---------------------------------------------------------------- extend
 @pytest.mark.parametrize("H", [3, 16, 40, 128])
 @pytest.mark.parametrize("ps", [1, 48])
