@@ -1152,8 +1152,8 @@ int cache_table(const char* name, const void* kv_cache, const void* kv_scale, co
   if (kv_cache && !aligned16(kv_cache)) return fail(FP8MOE_EINVAL, "%s: kv_cache must be 16-byte aligned", name);
   if (static_cast<long long>(num_pages) * page_size >= (1ll << 31))
     return fail(FP8MOE_EUNSUPPORTED, "%s: num_pages x page_size must stay below 2^31", name);
-  if (static_cast<long long>(num_indices) * page_size >= (1ll << 31))
-    return fail(FP8MOE_EUNSUPPORTED, "%s: num_indices x page_size must stay below 2^31", name);
+  if (static_cast<long long>(num_indices) * page_size > (1ll << 31) - 256)   // (positions up to a tile's end)
+    return fail(FP8MOE_EUNSUPPORTED, "%s: num_indices x page_size must not exceed 2^31 - 256", name);
   *t = PageTable{kv_indptr, kv_indices, kv_last_page_lens, batch, num_pages, page_size, num_indices};
   return FP8MOE_OK;
 }

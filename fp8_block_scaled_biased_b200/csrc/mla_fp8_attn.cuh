@@ -13,8 +13,8 @@
 //   q / s = hi + lo / 16, s a power of two per (query, head): hi is q / s rounded, and the
 //     rest of an 8-bit significand is exactly a 4-bit one (until lo falls to subnormals,
 //     2^-13 below the row's largest entry). N = 2 x columns.
-//   p = hi + lo / 32 + lo2 / 1024: 12 bits, down to 2^-25 of the largest weight, so that a
-//     long faint context beside one dominant token keeps its mass. N = 3 x columns.
+//   p = hi + lo / 32 + lo2 / 1024: off by 2^-14 of itself or 2^-22 of the largest weight, so that
+//     a long faint context beside one dominant token keeps its mass. N = 3 x columns.
 // Products of codes are exact and the MMA sums in fp32. Scales of pages (one per token row,
 // i.e. per TMEM lane) multiply the scores, and the weights before they are split.
 //
@@ -48,9 +48,9 @@ constexpr int kLatRot = kLatTile * 64;                     // the rotary bytes o
 constexpr int kLatMaxCtas = 148;                           // one per SM
 // A weight's code runs up to 2^8 (of 448). Its column's reference stands at 2^2, so a score may pass the
 // reference by 6 (base 2) before it has to move, which happens in about one tile of a hundred (of five,
-// with 4); what falls below 2^-22 of the reference is lost, at most a half of its size and at most
-// 2^-22 each. Longer contexts, whose references settle early on, get a higher reference, so that all
-// their tokens together lose less than 2^-8: half a step of the bf16 output.
+// with 4). The smallest step of a code is 2^-19 (lo2's), so a weight is off by at most 2^-22 of the
+// reference. Longer contexts, whose references settle early on, get a higher one, so that up to 2^18
+// tokens together lose less than 2^-8 of it: half a step of the bf16 output.
 __device__ __forceinline__ float lat_ref_exponent(int len) { return len <= (1 << 14) ? 2.0f : len <= (1 << 16) ? 4.0f : 6.0f; }
 constexpr float kLatTopExp = 8.0f;
 constexpr float kLatNoRef = 1e30f;                         // reference of a column that has none: any score passes it
@@ -93,8 +93,8 @@ struct LatSmem {
   static constexpr int kQBytes = kQRows * kLatDk;
   static constexpr int kPBytes = kPRows * kLatTile;
   // What shared memory holds: 2.5 tiles in halves (with 2, 64 x 8192 tokens on 16 heads took 78 us
-  // instead of 73, and chunks of 500 queries on 16 heads 223 instead of PERF3), the rotary bytes of two,
-  // the queries' terms, and the weights of two tiles, or of one beside 32 columns' queries.
+  // instead of 73), the rotary bytes of two, the queries' terms, and the weights of two tiles, or of
+  // one beside 32 columns' queries.
   static constexpr int kHalves = 5, kRots = 2, kPBufs = HG == 16 ? 2 : 1;
   static constexpr int kAhead = HG == 16 ? 4 : 2;          // tiles whose page-table entries are fetched ahead
   static constexpr int kOffRot = kHalves * kLatHalf;
@@ -1010,7 +1010,7 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     mbar_init(&s->q_full, kGroups);
     s->abort = 0;
     fence_mbar_init();
-    if constexpr (!SMALL) {
+    if (!SMALL && a.table.num_indices > 0) {              // (an empty table comes without maps)
       prefetch_tensormap(&tm_lat);
       prefetch_tensormap(&tm_rot);
     }

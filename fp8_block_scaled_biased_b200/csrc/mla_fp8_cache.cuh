@@ -126,14 +126,15 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
   const int lo = __ldg(a.append_indptr + b), hi = __ldg(a.append_indptr + b + 1);
   int first, len;
   const bool table = sequence_extent(a.table, b, first, len);
-  if (lo < 0 || hi < lo || hi > a.T || (table && hi - lo > len)) {
+  const long long nth = blockIdx.x - (lo / ps + 2ll * b);    // negative only where the ranges decrease
+  if (lo < 0 || hi < lo || hi > a.T || nth < 0 || (table && hi - lo > len)) {
     if (tid == 0) raise_device_error(FP8MOE_DEVERR_PAGE);
     return;
   }
   if (!table || hi == lo) return;
   const int start = len - (hi - lo);                         // position of the first new token
-  const int j = start / ps + static_cast<int>(blockIdx.x - (lo / ps + 2ll * b));
-  if (j > (len - 1) / ps) return;
+  if (start / ps + nth > (len - 1) / ps) return;
+  const int j = start / ps + static_cast<int>(nth);
   const int pos0 = max(start, j * ps);                       // (j * ps <= len - 1: no overflow)
   const int slot0 = pos0 - j * ps;
   const int rows = static_cast<int>(min(static_cast<long long>(len), (j + 1ll) * ps) - pos0);

@@ -624,12 +624,13 @@ int mla_decode_fwd(const uint16_t* q, const uint16_t* kv_buffer, uint16_t* o,
  *                (a page) and KV head. mla_kv_append_fp8 writes powers of two: the smallest
  *                s >= 2^-110 with amax <= 448 s, amax over the page's finite entries, 0 for
  *                a page whose finite entries are all zero. The attention and gather calls
- *                take any finite scale >= 0.
+ *                take any finite scale >= 0; the softmax weights keep the precision stated
+ *                below for scales of 0 and from 2^-90 to 2^100.
  *   kv_indptr, kv_indices, kv_last_page_lens: the page table, as for mla_decode_fwd.
  *                Sequence b holds L_b = (pages - 1) * page_size + kv_last_page_lens[b] tokens
  *                (0 without a page). Any page_size >= 1.
- * Limits of all four calls: batch <= 2^20; num_pages * page_size and num_indices *
- * page_size below 2^31. A page-table entry, or an append, query or output range, that is
+ * Limits of all four calls: batch <= 2^20; num_pages * page_size below 2^31, num_indices *
+ * page_size up to 2^31 - 256. A page-table entry, or an append, query or output range, that is
  * out of range is neither read nor written through: the device error word gets
  * FP8MOE_DEVERR_PAGE and that sequence's output is unspecified. All are deterministic.
  */
@@ -679,10 +680,12 @@ int mla_kv_gather_fp8(const uint8_t* kv_cache, const float* kv_scale,
  *   workspace  mla_fp8_workspace(num_heads, batch) bytes, 16-byte aligned; it needs no
  *              initialisation and keeps nothing between calls. Calls that may overlap on
  *              the GPU (other streams, other captured graphs) need one each.
- * No query is rounded: a bf16 entry is the sum of two e4m3 codes (below 2^-14 of its row's
- * largest magnitude: to 2^-22 of that). The softmax weights that multiply the values are
- * rounded to the sum of three e4m3 codes; the sum that divides them, and lse, are not.
- * An infinite query entry counts as NaN.
+ * No query is rounded: a bf16 entry is the sum of two e4m3 codes (below 2^-13 of its row's
+ * largest magnitude: to 2^-21 of that). The softmax weights that multiply the values are
+ * rounded to the sum of three e4m3 codes, off by at most 2^-14 of themselves or 2^-22 of the
+ * largest weight times scale (2^-24 in contexts above 2^14 tokens, 2^-26 above 2^16); the sum
+ * that divides them, and lse, are not rounded. An infinite query entry counts as NaN. A NaN
+ * in a cached row reaches every query that sees the row, and no other.
  */
 size_t mla_fp8_workspace(int num_heads, int num_q);
 int mla_decode_fp8_fwd(const uint16_t* q, const uint8_t* kv_cache, const float* kv_scale,

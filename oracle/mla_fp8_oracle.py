@@ -96,19 +96,24 @@ def gather(codes, scales, kv_indptr, kv_indices, out_indptr, out):
 
 
 def extend(q, qo_indptr, codes, scales, kv_indptr, kv_indices, kv_last_page_lens, sm_scale=None, logit_cap=0.0):
-    """o [T, H, 512], lse [T, H], and for error bounds mag = sum_j p_j |v_j| [T, H, 512] and
-    size = max_j sm_scale * <|q|, |k_j|> [T, H]; fp64. Rows of no sequence are NaN."""
+    """o [T, H, 512], lse [T, H], and for error bounds mag = sum_j p_j |v_j| [T, H, 512], size =
+    max_j sm_scale * <|q|, |k_j|> [T, H] and coded = max_j (p_j s_j) sum_j |v_j / s_j| [T, H, 512]
+    (s_j the scale of token j's page); fp64. Rows of no sequence are NaN."""
     T, H, Dk = q.shape
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(Dk)
     o = torch.full((T, H, 512), math.nan, dtype=F64)
     lse = torch.full((T, H), math.nan, dtype=F64)
-    mag, size = torch.zeros_like(o), torch.zeros_like(lse)
+    mag, size, coded = torch.zeros_like(o), torch.zeros_like(lse), torch.zeros_like(o)
     for b, L in enumerate(lengths(kv_indptr, kv_last_page_lens, codes.shape[1])):
         lo, hi = int(qo_indptr[b]), int(qo_indptr[b + 1])
         if hi == lo:
             continue
         kv = sequence_values(codes, scales, kv_indptr, kv_indices, b, L)
+        first, ps = int(kv_indptr[b]), codes.shape[1]
+        pages = [int(kv_indices[first + i // ps]) for i in range(L)]
+        sc = scales[pages, 0].to(F64)
+        sums = e4m3_decode(codes[pages, [i % ps for i in range(L)], 0, :512]).to(F64).abs().cumsum(0)
         for i in range(hi - lo):
             sees = max(0, L - (hi - lo) + i + 1)
             t = lo + i
@@ -125,8 +130,9 @@ def extend(q, qo_indptr, codes, scales, kv_indptr, kv_indices, kv_last_page_lens
             o[t] = (e / den) @ k[:, :512]
             mag[t] = (e / den) @ k[:, :512].abs()
             lse[t] = m[:, 0] + torch.log(den[:, 0])
+            coded[t] = (e / den * sc[:sees]).max(dim=1, keepdim=True).values * sums[sees - 1]
             size[t] = sm_scale * (q[t].to(F64).abs() @ k.abs().T).max(1).values
-    return o, lse, mag, size
+    return o, lse, mag, size, coded
 
 
 def decode(q, codes, scales, kv_indptr, kv_indices, kv_last_page_lens, sm_scale=None, logit_cap=0.0):

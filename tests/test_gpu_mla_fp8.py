@@ -11,13 +11,16 @@ Attention, from the kernel's arithmetic. With S = sm_scale * max_j <|q|, |k_j|>:
     the argument, itself within 2 S) below 2^-17 (1 + S);
   * so a softmax weight and its normaliser are each off by 2^-17 (1 + S), together
     2^-16 (1 + S) relatively;
-  * a weight times its page's scale is the sum of three e4m3 codes: 2^-12 relatively, or
-    2^-25 of the running largest one: at most 2^-24 L of the result's magnitude in all
-    (the largest weight is at least 1/L of the sum when the values are of one size; the
-    tests with pages of very different scales have L <= 512 and large codes of their own);
+  * a weight times its page's scale becomes three e4m3 codes, hi + lo / 32 + lo2 / 1024. Each
+    term halves a step of four significant bits: 2^-4, then 2^-5 of that (the rest is at most
+    2^-4 of 2^e, times 32 at most 2^(e+1)) and again: 2^-14 relatively, well inside 2^-12. Where
+    lo2 is subnormal (steps of 2^-9 / 1024 = 2^-19) the error is 2^-20 absolutely. The reference
+    is coded as 2^2 (2^4 above 2^14 tokens, 2^6 above 2^16), and nothing that set it is larger
+    than the largest weight times scale, M = max_j p_j s_j: 2^-22 M (2^-24, 2^-26) a token, and
+    with the codes v_j / s_j that it multiplies `faint` = 2^-22 M sum_j |v_j / s_j| in all;
   * fp32 sums of L/32 steps: L * 2^-28;
   * the bf16 output: half a step, 2^-8 relatively.
-|o - o_ref| <= (2^-16 (1 + S) + 2^-12 + 2^-23 L) * sum_j p_j |v_j| + 2^-8 |o_ref| + 1e-30,
+|o - o_ref| <= (2^-16 (1 + S) + 2^-12 + 2^-28 L) * sum_j p_j |v_j| + faint + 2^-8 |o_ref| + 1e-30,
 |lse - lse_ref| <= 2^-17 (1 + S) + 2^-21 (1 + |lse_ref|).
 """
 import ctypes
@@ -85,13 +88,17 @@ def _codes(t):
     return t.view(torch.uint8).cpu()
 
 
+def _bound(ref, mag, size, coded, L):
+    c = 2.0 ** -16 * (1 + size) + 2.0 ** -12 + 2.0 ** -28 * L
+    faint = 2.0 ** (-22 if L <= 2 ** 14 else -24 if L <= 2 ** 16 else -26)
+    return c[..., None] * mag + faint * coded + 2.0 ** -8 * ref.abs() + 1e-30
+
+
 def _check(b, q, qo, o, lse, **kw):
-    ref, ref_lse, mag, size = M8.extend(q, qo, b.codes, b.scales, *b.table, **kw)
+    ref, ref_lse, mag, size, coded = M8.extend(q, qo, b.codes, b.scales, *b.table, **kw)
     o, lse = o.cpu().double(), lse.cpu().double()
     rows = ~torch.isnan(ref_lse)
-    L = max(b.lens)
-    c = 2.0 ** -16 * (1 + size) + 2.0 ** -12 + 2.0 ** -23 * L
-    bound = c[..., None] * mag + 2.0 ** -8 * ref.abs() + 1e-30
+    bound = _bound(ref, mag, size, coded, max(b.lens))
     assert torch.isfinite(o[rows]).all()
     d = (o - ref).abs()
     worst = (d / bound)[rows].max().item()
@@ -193,6 +200,19 @@ def test_append_and_gather_of_nothing():
 
 
 # ---------------------------------------------------------------- gather
+@pytest.mark.parametrize("ld, off", [(576, 0), (584, 0), (592, 0), (592, 8), (640, 24)])
+def test_gather_into_rows_of_any_stride_and_alignment(ld, off):
+    b = Batch([70, 0, 33], 16, seed=3).device()
+    ip = _indptr([70, 0, 30])
+    buf = torch.full((100 * ld + 64,), 5.0, dtype=torch.bfloat16, device=DEV)
+    out = torch.as_strided(buf, (100, 576), (ld, 1), off)
+    B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, ip.to(DEV), out)
+    want = M8.gather(b.codes, b.scales, b.indptr, b.indices, ip, torch.full((100, 576), 5.0, dtype=torch.bfloat16))
+    assert torch.equal(out.cpu(), want)
+    out.fill_(5.0)
+    assert (buf == 5.0).all()                              # nothing between the rows
+
+
 @pytest.mark.parametrize("ps", [1, 7, 64])
 def test_gather_matches_the_oracle_and_leaves_other_rows(ps):
     lens, take = [5, 0, 70, 33, 64, 1], [5, 0, 41, 33, 0, 1]
@@ -304,10 +324,43 @@ def test_decode_nan_stays_with_its_sequence_and_head():
     want[1] = True
     assert torch.equal(nan, want)
     assert torch.equal(torch.isnan(o.cpu()).all(2), want) and torch.equal(torch.isnan(o.cpu()).any(2), want)
-    ref, ref_lse, mag, size = M8.decode(torch.nan_to_num(q, posinf=0.0), b.codes, b.scales, *b.table)
+    ref, ref_lse, mag, size, coded = M8.decode(torch.nan_to_num(q, posinf=0.0), b.codes, b.scales, *b.table)
     fine = ~want
-    bound = (2.0 ** -16 * (1 + size) + 2.0 ** -12 + 2.0 ** -23 * 200)[..., None] * mag + 2.0 ** -8 * ref.abs() + 1e-30
+    bound = _bound(ref, mag, size, coded, 200)
     assert ((o.cpu().double() - ref).abs()[fine] <= bound[fine]).all()
+
+
+@pytest.mark.parametrize("L, H, ps", [(17000, 3, 64), (17000, 40, 16), (70000, 2, 128), (70000, 1, 8)])
+def test_decode_long_contexts(L, H, ps):
+    """Contexts long enough for the two higher references, joined from a hundred and more parts; one
+    token stands 9 nats above the rest, so that most of the mass lies in faint weights."""
+    b = Batch([L], ps, seed=L + H, scale_exp=(-6, -6))
+    lat = b.codes.view(-1, 576)
+    lat[:, 575] = e4m3_encode(torch.zeros(1))
+    lat[int(b.indices[0]) * ps, 575] = e4m3_encode(torch.full((1,), 256.0))
+    b.device()
+    q = torch.zeros(1, H, 576)
+    q[:, :, 575] = 9.0 * 24 / (256 * 2.0 ** -6)
+    q[:, :, :8] = torch.randn(1, H, 8, generator=b.g) * 0.5
+    q = q.to(torch.bfloat16)
+    o, lse = _decode(b, q)
+    _check(b, q, torch.arange(2), o, lse)
+
+
+def test_decode_and_gather_of_a_shared_prefix():
+    """Two sequences whose tables begin with the same pages, and one that names a page twice."""
+    b = Batch([200, 90, 64], 32, seed=17)
+    b.indices[7:9] = b.indices[:2]
+    b.indices[11] = b.indices[10]
+    b.codes[b.indices.long()] = e4m3_encode(torch.randn(12, 32, 1, 576, generator=b.g) * 40)
+    b.device()
+    q = b.q(3, 16)
+    o, lse = _decode(b, q)
+    _check(b, q, torch.arange(4), o, lse)
+    out = torch.zeros(354, 576, dtype=torch.bfloat16, device=DEV)
+    ip = _indptr(b.lens)
+    B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, ip.to(DEV), out)
+    assert torch.equal(out.cpu(), M8.gather(b.codes, b.scales, b.indptr, b.indices, ip, torch.zeros_like(out).cpu()))
 
 
 @pytest.mark.parametrize("H, bad", [(8, 0), (5, 0), (16, 3), (24, 17)])
@@ -350,7 +403,7 @@ def test_decode_scales_at_the_ends_of_their_range():
     q = torch.zeros(1, 16, 576)
     q[:, :, 575] = 2.0 ** 103 * 5.75 * math.log(2.0)
     q = q.to(torch.bfloat16)
-    ref, ref_lse, _, size = M8.decode(q, b.codes, b.scales, *b.table, sm_scale=1.0)
+    ref, ref_lse, _, size, _ = M8.decode(q, b.codes, b.scales, *b.table, sm_scale=1.0)
     many = 160                                             # so many on the same pages that none is cut up
     b.dt = (torch.arange(many + 1, dtype=torch.int32, device=DEV) * 25, b.dt[1].repeat(many), b.dt[2].repeat(many))
     o, lse = _decode(b, q.expand(many, 16, 576).contiguous(), sm_scale=1.0)
@@ -365,6 +418,17 @@ def test_decode_scales_at_the_ends_of_their_range():
 
 
 # ---------------------------------------------------------------- extend
+@pytest.mark.parametrize("ps", [2, 8, 16, 32, 96, 128, 256])
+@pytest.mark.parametrize("H", [5, 48])
+def test_extend_by_page_size(ps, H):
+    b = Batch([129, 1, 400, 128, 257], ps, seed=ps + H).device()
+    new = [9, 1, 4, 0, 13]
+    qo = _indptr(new)
+    q = b.q(sum(new), H)
+    o, lse = _extend(b, q, qo)
+    _check(b, q, qo, o, lse)
+
+
 @pytest.mark.parametrize("H", [3, 16, 40, 128])
 @pytest.mark.parametrize("ps", [1, 48])
 def test_extend_ragged(ps, H):
@@ -414,9 +478,9 @@ def test_extend_a_nan_token_stays_hidden_from_earlier_queries():
     clean = Batch([140, 20], 16, seed=4)
     clean.codes = b.codes.clone()
     clean.codes[page, 135 % 16, 0, 300] = 0x20
-    ref, ref_lse, mag, size = M8.extend(q, qo, clean.codes, clean.scales, *clean.table)
+    ref, ref_lse, mag, size, coded = M8.extend(q, qo, clean.codes, clean.scales, *clean.table)
     fine = ~nan
-    bound = (2.0 ** -16 * (1 + size) + 2.0 ** -12 + 2.0 ** -23 * 140)[..., None] * mag + 2.0 ** -8 * ref.abs() + 1e-30
+    bound = _bound(ref, mag, size, coded, 140)
     assert ((o.cpu().double() - ref).abs()[fine] <= bound[fine]).all()
 
 
@@ -522,6 +586,28 @@ def test_captured_step_replays_on_new_contents():
         _check(b, qs, torch.arange(3), o, lse)
 
 
+def test_two_captured_graphs_share_a_workspace():
+    b = Batch([700, 30, 300], 64, seed=52).device()
+    ws = torch.empty(B.mla_fp8_workspace_bytes(128, 3), dtype=torch.uint8, device=DEV)
+    runs = []
+    for H in (16, 128):
+        q = b.q(3, H).to(DEV)
+        o = torch.zeros(3, H, 512, dtype=torch.bfloat16, device=DEV)
+        want = _decode(b, q)[0]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            B.mla_decode_fp8_fwd(q, b.dc, b.ds, o, *b.dt, workspace=ws)
+        runs.append((g, q, o, want))
+    for _ in range(5):
+        for g, _, o, _ in runs:
+            o.zero_()
+            g.replay()
+    for _, _, o, want in runs:
+        assert torch.equal(o, want)
+
+
 def test_two_streams_with_a_workspace_each():
     b = Batch([900, 411, 1300], 16, seed=50).device()
     q = b.q(3, 32)
@@ -616,3 +702,19 @@ def test_ranges_out_of_bounds_are_flagged_not_followed():
     rows = torch.zeros(22, 576, dtype=torch.bfloat16, device=DEV)
     B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, ip, rows)
     assert B.device_status() == 32 and (rows[20] == 0).all()
+
+
+def test_append_ranges_that_decrease_are_flagged():
+    """A later range that begins before an earlier one: no page before a sequence's first is looked up."""
+    b = Batch([60, 60, 60, 60], 1, seed=72, poison=False).device()
+    x = torch.ones(60, 576, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_append_fp8(x, torch.tensor([0, 50, 55, 3, 9], dtype=torch.int32, device=DEV), b.dc, b.ds, *b.dt)
+    assert B.device_status() == 32
+
+
+def test_decode_of_an_empty_table():
+    for H in (16, 128):
+        b = Batch([0, 0], 64, seed=73).device()
+        assert b.dt[1].numel() == 0
+        o, lse = _decode(b, b.q(2, H))
+        assert (o == 0).all() and torch.isneginf(lse).all()

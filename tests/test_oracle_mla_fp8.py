@@ -64,7 +64,7 @@ def test_attention_equals_the_bf16_oracle_on_exact_values_and_is_causal():
     scales = torch.full((6, 1), 2.0 ** -4)
     q = torch.randn(4, H, 576, generator=g).to(torch.bfloat16)
     table = _table(L, ps, [5, 0, 3, 1])
-    o, lse, mag, _ = M8.extend(q, [0, 4], codes, scales, *table, logit_cap=3.0)
+    o, lse, mag, _, _ = M8.extend(q, [0, 4], codes, scales, *table, logit_cap=3.0)
     values = e4m3_decode(codes) * 2.0 ** -4
     for i in range(4):
         ref, ref_lse = M.mla_decode(q[i:i + 1], values, *_table(L - 3 + i, ps, [5, 0, 3, 1]), logit_cap=3.0)
@@ -76,7 +76,7 @@ def test_queries_before_the_first_token_see_nothing_and_gather_rounds_once():
     codes = torch.full((1, 2, 1, 576), 0x39, dtype=torch.uint8)                     # 1.125
     scales = torch.tensor([[0.5]])
     q = torch.ones(3, 1, 576, dtype=torch.bfloat16)
-    o, lse, _, _ = M8.extend(q, [0, 3], codes, scales, *_table(2, 2, [0]))
+    o, lse, *_ = M8.extend(q, [0, 3], codes, scales, *_table(2, 2, [0]))
     assert (o[0] == 0).all() and lse[0, 0] == -math.inf
     assert o[1, 0, 0] == 0.5625 and lse[1, 0].item() == pytest.approx(576 * 0.5625 / 24)
     out = M8.gather(codes, scales, [0, 1], [0], [1, 3], torch.full((4, 576), 7.0, dtype=torch.bfloat16))
