@@ -219,14 +219,14 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 // Whether a phase has completed, without waiting for it (try_wait may suspend the thread).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_test_at(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
 }
@@ -697,8 +697,10 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
 // ---------------------------------------------------------------- MMA warp
 // The whole warp runs the loop and one elected lane issues, so that descriptors stay in uniform
 // registers: 44 and 48 cycles per MMA (16 columns), 70 from a divergent branch. Every turn asks all
-// barriers that matter at once, a lane each: the halves of the next tile's rows, its score buffer,
-// this tile's weights. A half of a tile is scored as soon as it is there.
+// barriers that matter at once, a lane each: the half of the next tile's rows, its score buffer,
+// this tile's weights. A half of a tile is scored as soon as it is there. With 32 columns this warp
+// is the bottleneck: a tile's MMAs take 1770 cycles, a turn between them 300 if it finds its
+// places by division, which cost chunks of 500 queries on 16 heads 191 us instead of 182.
 template <int HG>
 __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint8_t* smem, uint32_t tmem_any) {
   using SM = LatSmem<HG>;
@@ -714,7 +716,13 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
   const uint64_t desc_v = umma_desc(base, 1024, 1024, 2);                          // the same rows, M-major
   const uint64_t desc_p = umma_desc(base + SM::kOffP, 128, 16 * kLatTile, 0);
   const bool leader = elect_one();
-  int it0 = 0, fslot = 0, fcount = 0;
+  static_assert(SM::kRots == 2, "rotary bytes lie in the place of the score buffer's number");
+  const uint32_t bars_kv = smem_u32(s->kv_full), bars_s = smem_u32(s->s_empty), bars_p = smem_u32(s->p_full);
+  // lanes ask a barrier each: 0 the rows of the next half to be scored, 1 its score buffer, others the weights
+  uint32_t bar = lane == 0 ? bars_kv : lane == 1 ? bars_s : bars_p;
+  uint32_t parity = lane == 1 ? 1u : 0u;
+  int kslot = 0, vslot = 0, buf = 0, pbuf = 0;             // places of what is scored next, and multiplied with V
+  int fslot = 0, fcount = 0;
   uint32_t fphase = 0;
   for (;;) {
     if (!__all_sync(0xffffffffu, lat_wait(&s->frag_full[fslot], fphase, abort_flag))) return false;
@@ -724,30 +732,33 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
     if (n == 0) return true;
     if (!__all_sync(0xffffffffu, lat_wait(&s->q_full, fcount & 1, abort_flag))) return false;
     ++fcount;
-    int qk = 0, pv = 0;                                    // halves of tiles scored, tiles multiplied with V
+    int left_qk = 2 * n, left_pv = n, ahead = 0;           // halves to score, tiles to multiply with V, halves scored ahead of V
+    uint32_t spin = 0;
     unsigned long long t0 = 0;
-    for (uint32_t spin = 0; pv < n; ++spin) {
-      const int i = it0 + (qk >> 1), buf = i & 1, half = qk & 1;
-      const int j = it0 + pv, pbuf = j % SM::kPBufs;
-      const LatHalf h = lat_half<SM::kHalves>(2 * i + half);
-      uint64_t* bar = lane == 0 ? &s->kv_full[h.slot] : lane == 1 ? &s->s_empty[buf] : &s->p_full[pbuf];
-      const uint32_t parity = lane == 0 ? h.phase : lane == 1 ? ((i >> 1) & 1) ^ 1u : (j / SM::kPBufs) & 1;
-      uint32_t ready = __ballot_sync(0xffffffffu, mbar_test(bar, parity));
-      if (half) ready |= 2u;                               // the score buffer is this tile's already
-      const bool do_qk = qk < 2 * n && qk <= 2 * pv + 3 && (ready & 3u) == 3u;
-      const bool do_pv = 2 * pv + 2 <= qk && (ready & 4u) != 0;
-      if (do_qk || do_pv) tc_fence_after();
+    while (left_pv > 0) {
+      const uint32_t ready = __ballot_sync(0xffffffffu, mbar_test_at(bar, parity));
+      const bool second = ahead & 1;                       // (its score buffer is this tile's already)
+      const bool do_qk = left_qk > 0 && ahead < 4 && (ready & 3u) == 3u;
+      const bool do_pv = ahead >= 2 && (ready & 4u) != 0;
+      if (!(do_qk || do_pv)) {
+        if (++spin == 64) t0 = global_timer_ns();
+        if ((spin & 1023u) == 1023u && __any_sync(0xffffffffu, *abort_flag || global_timer_ns() - t0 > kWaitLimitNs))
+          return false;
+        continue;
+      }
+      spin = 0;
+      tc_fence_after();
       // scores first: the softmax warps wait for them, and a half takes the MMAs half as long as P V
       if (do_qk) {
         if (leader) {
           const uint32_t d = tmem + SM::kTmemS + buf * SM::kQRows;
-          const uint64_t rows = desc_k + h.slot * (kLatHalf >> 4);
-          if (half == 0) {
-            const uint64_t rot = desc_rot + (static_cast<uint64_t>(i % SM::kRots * kLatRot) >> 4);
+          const uint64_t rows = desc_k + kslot * (kLatHalf >> 4);
+          if (!second) {
+            const uint64_t rot = desc_rot + buf * (kLatRot >> 4);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               umma_f8(d, rot + k * 2, desc_q + (32 + k * 2) * SM::kQRows, kIdescS, k > 0 ? 1u : 0u);
-            umma_commit(&s->rot_empty[i % SM::kRots]);
+            umma_commit(&s->rot_empty[buf]);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               umma_f8(d, rows + (k >> 2) * (kLatChunk >> 4) + (k & 3) * 2, desc_q + k * 2 * SM::kQRows, kIdescS, 1u);
@@ -759,14 +770,26 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
           }
         }
         __syncwarp();
-        ++qk;
-        spin = 0;
+        --left_qk;
+        ++ahead;
+        kslot = kslot == SM::kHalves - 1 ? 0 : kslot + 1;
+        if (lane == 0) {
+          bar = bars_kv + kslot * 8;
+          if (kslot == 0) parity ^= 1u;
+        }
+        if (second) {
+          buf ^= 1;
+          if (lane == 1) {
+            bar = bars_s + buf * 8;
+            if (buf == 0) parity ^= 1u;
+          }
+        }
       }
       if (do_pv) {
         if (leader) {
-          const int h0 = lat_half<SM::kHalves>(2 * j).slot, h1 = lat_half<SM::kHalves>(2 * j + 1).slot;
+          const int h0 = vslot, h1 = vslot == SM::kHalves - 1 ? 0 : vslot + 1;
           const uint64_t p = desc_p + (pbuf * (SM::kPBytes >> 4));
-          const uint32_t more = pv > 0 ? 1u : 0u;
+          const uint32_t more = left_pv < n ? 1u : 0u;
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
 #pragma unroll
@@ -779,14 +802,16 @@ __device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint
           umma_commit(&s->p_empty[pbuf]);
         }
         __syncwarp();
-        ++pv;
-        spin = 0;
+        --left_pv;
+        ahead -= 2;
+        vslot = vslot >= SM::kHalves - 2 ? vslot + 2 - SM::kHalves : vslot + 2;
+        if (SM::kPBufs == 2) pbuf ^= 1;
+        if (lane >= 2) {
+          bar = bars_p + pbuf * 8;
+          if (pbuf == 0) parity ^= 1u;
+        }
       }
-      if (spin == 64) t0 = global_timer_ns();
-      if ((spin & 1023u) == 1023u && __any_sync(0xffffffffu, *abort_flag || global_timer_ns() - t0 > kWaitLimitNs))
-        return false;
     }
-    it0 += n;
   }
 }
 
@@ -914,7 +939,7 @@ __device__ __forceinline__ bool lat_copy_role(const LatAttnArgs& a, const uint8_
     pending = -1;
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {        // announces what is pending before it has to wait
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_test_at(smem_u32(bar), parity))) return true;
     if (pending >= 0) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       announce();
