@@ -1301,12 +1301,12 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
   a.sm_scale = sm_scale;
   a.logit_cap = logit_cap;
   a.cache = kv_cache;
-  // Rows that a page holds together come by TMA boxes: the largest power of two in page_size. Below 16
-  // rows the boxes take longer to issue (80 cycles each, five per box of rows) than HBM needs for the
-  // tile (3250), and four warps copy the rows instead (64 x 8192 tokens, pages of 8: 81 us against 124;
-  // pages of 16: 81 against 80); with 16 columns, whose threads leave room for them.
+  // Rows that a page holds together come by TMA boxes: the largest power of two in page_size. Boxes of 8
+  // rows still keep up (64 x 8192 tokens on 16 heads: 73 us, as copied by four warps; 24 x 4096 on 128
+  // heads: 59 against 76, because the copying warps leave threads for 16 columns only); below that the
+  // rows of a box no longer fill the pattern that the MMAs read, and the four warps copy.
   a.run = std::min(kLatTile, page_size & -page_size);
-  const bool small = a.run < 16;
+  const bool small = a.run < 8;
   CUtensorMap lat, rot;
   std::memset(&lat, 0, sizeof(lat));
   std::memset(&rot, 0, sizeof(rot));

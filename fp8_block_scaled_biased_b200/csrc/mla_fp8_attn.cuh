@@ -20,7 +20,7 @@
 //
 // A CTA holds `HG` columns and walks 128-token tiles through a ring of half tiles in shared memory:
 //   warp 3      the work list (below) and the page table: the tiles' rows and scales, some tiles ahead
-//   warps 0, 2  TMA: boxes of 16 to 128 rows that a page holds together; one half of a tile each
+//   warps 0, 2  TMA: boxes of 8 to 128 rows that a page holds together; one half of a tile each
 //   warps 12-15 for smaller pages instead: 16-byte asynchronous copies
 //   warp 1      the MMAs: scores of the next tile are issued ahead of this tile's P V if its
 //               rows have landed, else after
@@ -67,7 +67,7 @@ struct LatAttnArgs {
   float2* part_ml;               // [2 * CTAs, HG]: reference and sum
   int4* merge;                   // [CTAs]: first row, columns, parts, first part's slot (parts 0: nothing)
   int num_q, Hq, gang_log;       // CTAs of a gang: 1, 2 or 4
-  int run;                       // rows per TMA box: 16 to 128
+  int run;                       // rows per TMA box: 8 to 128
   float sm_scale, logit_cap;
 };
 
@@ -872,7 +872,7 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
   }
 }
 
-// Warps 0 and 2, pages of 16 rows and more: TMA boxes, each warp one half of every tile (half 0: the
+// Warps 0 and 2, pages of 8 rows and more: TMA boxes, each warp one half of every tile (half 0: the
 // rotary entries and chunks 0, 1; half 1: chunks 2, 3) as P V frees them. As in the MMA warp all lanes
 // run the loop and one issues: a copy takes 80 cycles to issue beside the softmax warps, 100 to 150
 // from a divergent branch.
