@@ -20,13 +20,12 @@
 //
 // A CTA holds `HG` columns and walks 128-token tiles through a ring of half tiles in shared memory:
 //   warp 3      the work list (below) and the page table: the tiles' rows and scales, some tiles ahead
-//   warps 0, 2  TMA: boxes of 8 to 128 rows that a page holds together; one half of a tile each
+//   warp 0      TMA: boxes of 8 to 128 rows that a page holds together
 //   warps 12-15 for smaller pages instead: 16-byte asynchronous copies
-//   warp 1      the MMAs: scores of the next tile are issued ahead of this tile's P V if its
-//               rows have landed, else after
+//   warps 1, 2  the MMAs: of the scores, and of P V
 //   warps 4..   one warpgroup per 8 columns, a token per thread: online softmax. The running
-//               reference of a column only moves when a score passes it by more than one
-//               (base 2), and then the accumulators in TMEM are rescaled.
+//               reference of a column only moves when a weight would leave its code's range, and
+//               then the accumulators in TMEM are rescaled.
 //
 // Work list: the tiles of all (sequence, column group) pairs in one row, cut into equal
 // shares; a share may begin and end inside a pair. Pairs cut in parts leave unnormalised
@@ -694,123 +693,104 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
   }
 }
 
-// ---------------------------------------------------------------- MMA warp
-// The whole warp runs the loop and one elected lane issues, so that descriptors stay in uniform
-// registers: 44 and 48 cycles per MMA (16 columns), 70 from a divergent branch. Every turn asks all
-// barriers that matter at once, a lane each: the half of the next tile's rows, its score buffer,
-// this tile's weights. A half of a tile is scored as soon as it is there. With 32 columns this warp
-// is the bottleneck: a tile's MMAs take 1770 cycles, a turn between them 300 if it finds its
-// places by division, which cost chunks of 500 queries on 16 heads 191 us instead of 182.
+// ---------------------------------------------------------------- MMA warps
+// Scores and P V are issued by a warp each, so that one's waits pass while the other's MMAs run: with
+// both in one warp a tile of 32 columns took 3170 cycles, of which its MMAs 1770 and what lay between
+// them 670 (chunks of 500 queries on 16 heads: 182 us instead of 162). All lanes run the loops and one elected lane issues, so that descriptors stay in
+// uniform registers: 44 and 48 cycles per MMA (16 columns), 70 from a divergent branch.
 template <int HG>
-__device__ __forceinline__ bool lat_mma_role(typename LatSmem<HG>::Info* s, uint8_t* smem, uint32_t tmem_any) {
+__device__ __forceinline__ bool lat_score_role(typename LatSmem<HG>::Info* s, uint8_t* smem, uint32_t tmem_any) {
   using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
-  const int lane = threadIdx.x & 31;
-  constexpr uint32_t kIdescS = umma_idesc_e4m3_f32(128, SM::kQRows);
-  constexpr uint32_t kIdescO = umma_idesc_e4m3_f32(128, SM::kPRows) | (1u << 15) | (1u << 16);   // A and B M/N-major
+  constexpr uint32_t kIdesc = umma_idesc_e4m3_f32(128, SM::kQRows);
   const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   const uint64_t desc_k = umma_desc(base, 16, 1024, 2);                            // rows of 128 bytes, K-major
   const uint64_t desc_rot = umma_desc(base + SM::kOffRot, 16, 512, 4);             // rows of 64 bytes
   const uint64_t desc_q = umma_desc(base + SM::kOffQ, SM::kQRows * 16, 128, 0);
-  const uint64_t desc_v = umma_desc(base, 1024, 1024, 2);                          // the same rows, M-major
-  const uint64_t desc_p = umma_desc(base + SM::kOffP, 128, 16 * kLatTile, 0);
   const bool leader = elect_one();
   static_assert(SM::kRots == 2, "rotary bytes lie in the place of the score buffer's number");
-  const uint32_t bars_kv = smem_u32(s->kv_full), bars_s = smem_u32(s->s_empty), bars_p = smem_u32(s->p_full);
-  // lanes ask a barrier each: 0 the rows of the next half to be scored, 1 its score buffer, others the weights
-  uint32_t bar = lane == 0 ? bars_kv : lane == 1 ? bars_s : bars_p;
-  uint32_t parity = lane == 1 ? 1u : 0u;
-  int kslot = 0, vslot = 0, buf = 0, pbuf = 0;             // places of what is scored next, and multiplied with V
-  int fslot = 0, fcount = 0;
-  uint32_t fphase = 0;
+  int slot = 0, buf = 0, fslot = 0;                        // places of the next half and its scores
+  uint32_t phase = 0, buf_phase = 1, fphase = 0, q_phase = 0;
   for (;;) {
     if (!__all_sync(0xffffffffu, lat_wait(&s->frag_full[fslot], fphase, abort_flag))) return false;
     const int n = __shfl_sync(0xffffffffu, s->frag[fslot].valid ? s->frag[fslot].tile1 - s->frag[fslot].tile0 : 0, 0);
     if (leader) mbar_arrive(&s->frag_empty[fslot]);
     if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
     if (n == 0) return true;
-    if (!__all_sync(0xffffffffu, lat_wait(&s->q_full, fcount & 1, abort_flag))) return false;
-    ++fcount;
-    int left_qk = 2 * n, left_pv = n, ahead = 0;           // halves to score, tiles to multiply with V, halves scored ahead of V
-    uint32_t spin = 0;
-    unsigned long long t0 = 0;
-    while (left_pv > 0) {
-      const uint32_t ready = __ballot_sync(0xffffffffu, mbar_test_at(bar, parity));
-      const bool second = ahead & 1;                       // (its score buffer is this tile's already)
-      const bool do_qk = left_qk > 0 && ahead < 4 && (ready & 3u) == 3u;
-      const bool do_pv = ahead >= 2 && (ready & 4u) != 0;
-      if (!(do_qk || do_pv)) {
-        if (++spin == 64) t0 = global_timer_ns();
-        if ((spin & 1023u) == 1023u && __any_sync(0xffffffffu, *abort_flag || global_timer_ns() - t0 > kWaitLimitNs))
-          return false;
-        continue;
-      }
-      spin = 0;
-      tc_fence_after();
-      // scores first: the softmax warps wait for them, and a half takes the MMAs half as long as P V
-      if (do_qk) {
+    if (!__all_sync(0xffffffffu, lat_wait(&s->q_full, q_phase, abort_flag))) return false;
+    q_phase ^= 1u;
+    for (int t = 0; t < n; ++t) {
+      const uint32_t d = tmem + SM::kTmemS + buf * SM::kQRows;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        bool ok = lat_wait(&s->kv_full[slot], phase, abort_flag);
+        if (half == 0) ok = ok && lat_wait(&s->s_empty[buf], buf_phase, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
         if (leader) {
-          const uint32_t d = tmem + SM::kTmemS + buf * SM::kQRows;
-          const uint64_t rows = desc_k + kslot * (kLatHalf >> 4);
-          if (!second) {
-            const uint64_t rot = desc_rot + buf * (kLatRot >> 4);
+          if (half == 0) {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              umma_f8(d, rot + k * 2, desc_q + (32 + k * 2) * SM::kQRows, kIdescS, k > 0 ? 1u : 0u);
+              umma_f8(d, desc_rot + buf * (kLatRot >> 4) + k * 2, desc_q + (32 + k * 2) * SM::kQRows, kIdesc, k > 0 ? 1u : 0u);
             umma_commit(&s->rot_empty[buf]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_f8(d, rows + (k >> 2) * (kLatChunk >> 4) + (k & 3) * 2, desc_q + k * 2 * SM::kQRows, kIdescS, 1u);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_f8(d, rows + (k >> 2) * (kLatChunk >> 4) + (k & 3) * 2, desc_q + (16 + k * 2) * SM::kQRows, kIdescS, 1u);
-            umma_commit(&s->s_full[buf]);
           }
+          const uint64_t rows = desc_k + slot * (kLatHalf >> 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_f8(d, rows + (k >> 2) * (kLatChunk >> 4) + (k & 3) * 2, desc_q + (half * 16 + k * 2) * SM::kQRows, kIdesc, 1u);
+          if (half == 1) umma_commit(&s->s_full[buf]);
         }
         __syncwarp();
-        --left_qk;
-        ++ahead;
-        kslot = kslot == SM::kHalves - 1 ? 0 : kslot + 1;
-        if (lane == 0) {
-          bar = bars_kv + kslot * 8;
-          if (kslot == 0) parity ^= 1u;
-        }
-        if (second) {
-          buf ^= 1;
-          if (lane == 1) {
-            bar = bars_s + buf * 8;
-            if (buf == 0) parity ^= 1u;
+        if (++slot == SM::kHalves) { slot = 0; phase ^= 1u; }
+      }
+      buf ^= 1;
+      if (buf == 0) buf_phase ^= 1u;
+    }
+  }
+}
+
+template <int HG>
+__device__ __forceinline__ bool lat_value_role(typename LatSmem<HG>::Info* s, uint8_t* smem, uint32_t tmem_any) {
+  using SM = LatSmem<HG>;
+  volatile int* abort_flag = &s->abort;
+  constexpr uint32_t kIdesc = umma_idesc_e4m3_f32(128, SM::kPRows) | (1u << 15) | (1u << 16);   // A and B M/N-major
+  const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
+  const uint64_t desc_v = umma_desc(base, 1024, 1024, 2);                          // the scores' rows, M-major
+  const uint64_t desc_p = umma_desc(base + SM::kOffP, 128, 16 * kLatTile, 0);
+  const bool leader = elect_one();
+  int slot = 0, pbuf = 0, fslot = 0;
+  uint32_t phase = 0, fphase = 0;
+  for (;;) {
+    if (!__all_sync(0xffffffffu, lat_wait(&s->frag_full[fslot], fphase, abort_flag))) return false;
+    const int n = __shfl_sync(0xffffffffu, s->frag[fslot].valid ? s->frag[fslot].tile1 - s->frag[fslot].tile0 : 0, 0);
+    if (leader) mbar_arrive(&s->frag_empty[fslot]);
+    if (++fslot == 2) { fslot = 0; fphase ^= 1u; }
+    if (n == 0) return true;
+    for (int t = 0; t < n; ++t) {
+      if (!__all_sync(0xffffffffu, lat_wait(&s->p_full[pbuf], phase, abort_flag))) return false;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t p = desc_p + pbuf * (SM::kPBytes >> 4);
+        const uint32_t more = t > 0 ? 1u : 0u;
+        int half = slot;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f8(tmem + SM::kTmemO + m * SM::kPRows, desc_v + half * (kLatHalf >> 4) + (m & 1) * (kLatChunk >> 4) + k * 256,
+                    p + k * 32, kIdesc, k > 0 ? 1u : more);
+          if (m & 1) {
+            umma_commit(&s->kv_empty[half]);
+            half = half == SM::kHalves - 1 ? 0 : half + 1;
           }
         }
+        umma_commit(&s->p_empty[pbuf]);
       }
-      if (do_pv) {
-        if (leader) {
-          const int h0 = vslot, h1 = vslot == SM::kHalves - 1 ? 0 : vslot + 1;
-          const uint64_t p = desc_p + (pbuf * (SM::kPBytes >> 4));
-          const uint32_t more = left_pv < n ? 1u : 0u;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8(tmem + SM::kTmemO + m * SM::kPRows,
-                      desc_v + (m < 2 ? h0 : h1) * (kLatHalf >> 4) + (m & 1) * (kLatChunk >> 4) + k * 256, p + k * 32,
-                      kIdescO, k > 0 ? 1u : more);
-            if (m & 1) umma_commit(&s->kv_empty[m < 2 ? h0 : h1]);
-          }
-          umma_commit(&s->p_empty[pbuf]);
-        }
-        __syncwarp();
-        --left_pv;
-        ahead -= 2;
-        vslot = vslot >= SM::kHalves - 2 ? vslot + 2 - SM::kHalves : vslot + 2;
-        if (SM::kPBufs == 2) pbuf ^= 1;
-        if (lane >= 2) {
-          bar = bars_p + pbuf * 8;
-          if (pbuf == 0) parity ^= 1u;
-        }
-      }
+      __syncwarp();
+      slot = slot >= SM::kHalves - 2 ? slot + 2 - SM::kHalves : slot + 2;
+      if (++pbuf == SM::kPBufs) { pbuf = 0; phase ^= 1u; }
     }
   }
 }
@@ -872,16 +852,15 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
   }
 }
 
-// Warps 0 and 2, pages of 8 rows and more: TMA boxes, each warp one half of every tile (half 0: the
-// rotary entries and chunks 0, 1; half 1: chunks 2, 3) as P V frees them. As in the MMA warp all lanes
-// run the loop and one issues: a copy takes 80 cycles to issue beside the softmax warps, 100 to 150
-// from a divergent branch.
-template <int HG, int half>
+// Warp 0, pages of 8 rows and more: TMA boxes, half by half (half 0: the rotary entries and chunks 0, 1;
+// half 1: chunks 2, 3) as P V frees them. One lane reads the rows, four at a time, and issues: boxes of
+// 16 rows then take 30 cycles each. With a shuffle per row by the whole warp they took 80, and bound
+// chunks of 33 queries on 128 heads in pages of 16: 153 us instead of 137.
+template <int HG>
 __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtensorMap* tm_lat, const CUtensorMap* tm_rot,
                                               typename LatSmem<HG>::Info* s, uint8_t* smem) {
   using SM = LatSmem<HG>;
   volatile int* abort_flag = &s->abort;
-  const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   const int run = a.run, pieces = kLatTile / run;
   const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
@@ -892,28 +871,35 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
     if (!__all_sync(0xffffffffu, lat_wait(&s->rows_full[ahead], (it / SM::kAhead) & 1, abort_flag))) return false;
     const int live = __shfl_sync(0xffffffffu, s->live[ahead], 0);
     if (live < 0) return true;
-    const int mine = s->rows[ahead][lane];
-    __syncwarp();
-    if (leader) mbar_arrive(&s->tab_empty[ahead]);
-    const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
-    bool ok = lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag);
-    if (half == 0) ok = ok && lat_wait(&s->rot_empty[it % SM::kRots], ((it / SM::kRots) & 1) ^ 1u, abort_flag);
-    if (!__all_sync(0xffffffffu, ok)) return false;
-    const uint32_t full = bars + h.slot * 8;
-    uint32_t dst = base + h.slot * kLatHalf, rot = base + SM::kOffRot + it % SM::kRots * kLatRot;
-    if (leader) mbar_arrive_expect_tx(&s->kv_full[h.slot], live * (half == 0 ? 320 : 256));
-#pragma unroll 2
-    for (int i = 0; i < pieces; ++i) {
-      const int row = __shfl_sync(0xffffffffu, mine, i);
-      if (row >= 0 && leader) {
-        tma_load_at(dst, lat, full, half * 256, row);
-        tma_load_at(dst + kLatChunk, lat, full, half * 256 + 128, row);
-        if (half == 0) tma_load_at(rot, rotary, full, 512, row);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const LatHalf h = lat_half<SM::kHalves>(2 * it + half);
+      bool ok = lat_wait(&s->kv_empty[h.slot], h.phase ^ 1u, abort_flag);
+      if (half == 0) ok = ok && lat_wait(&s->rot_empty[it % SM::kRots], ((it / SM::kRots) & 1) ^ 1u, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (leader) {
+        const uint32_t full = bars + h.slot * 8;
+        uint32_t dst = base + h.slot * kLatHalf, rot = base + SM::kOffRot + it % SM::kRots * kLatRot;
+        mbar_arrive_expect_tx(&s->kv_full[h.slot], live * (half == 0 ? 320 : 256));
+#pragma unroll 1
+        for (int i = 0; i < pieces; i += 4) {
+          const int4 r4 = *reinterpret_cast<const int4*>(&s->rows[ahead][i]);
+          const int r[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (r[k] >= 0) {
+              tma_load_at(dst, lat, full, half * 256, r[k]);
+              tma_load_at(dst + kLatChunk, lat, full, half * 256 + 128, r[k]);
+              if (half == 0) tma_load_at(rot, rotary, full, 512, r[k]);
+            }
+            dst += run * 128;
+            rot += run * 64;
+          }
+        }
+        if (half == 1) mbar_arrive(&s->tab_empty[ahead]);
       }
-      dst += run * 128;
-      rot += run * 64;
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
@@ -1025,12 +1011,12 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->s_empty[i], 4 * kGroups);
       mbar_init(&s->frag_full[i], 1);
-      mbar_init(&s->frag_empty[i], 1 + 4 * kGroups);
+      mbar_init(&s->frag_empty[i], 2 + 4 * kGroups);
     }
     for (int i = 0; i < SM::kAhead; ++i) {
       mbar_init(&s->rows_full[i], 1);
       mbar_init(&s->scale_full[i], 1);
-      mbar_init(&s->tab_empty[i], (SMALL ? 4 : 2) + 4 * kGroups);
+      mbar_init(&s->tab_empty[i], (SMALL ? 4 : 1) + 4 * kGroups);
     }
     mbar_init(&s->q_full, kGroups);
     s->abort = 0;
@@ -1094,17 +1080,19 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     if (threadIdx.x == 0) a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (SMALL && warp >= 4 + 4 * kGroups) {
     ok = lat_copy_role<HG>(a, a.cache, s, smem);
+  } else if (warp == 2) {
+    ok = lat_value_role<HG>(s, smem, tmem);
   } else if (warp >= 4) {
     ok = lat_softmax_role<HG>(a, s, smem, tmem);
   } else if (warp == 1) {
-    ok = lat_mma_role<HG>(s, smem, tmem);
+    ok = lat_score_role<HG>(s, smem, tmem);
   } else if (warp == 3) {
     LatSchedule<HG> schedule{s->start, s->start_b,  s->start_off, p0, p0, lat_div(total * (gang_id + 1), ngangs), total,
                              ngangs,   gang_id,     rank,         make_int4(0, 0, 0, 0)};
     ok = lat_table_role<HG, SMALL>(a, s, schedule);
     if (!ok && lane == 0) a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);   // the joining kernel must not find old words
   } else if constexpr (!SMALL) {
-    ok = warp == 0 ? lat_load_role<HG, 0>(a, &tm_lat, &tm_rot, s, smem) : lat_load_role<HG, 1>(a, &tm_lat, &tm_rot, s, smem);
+    ok = lat_load_role<HG>(a, &tm_lat, &tm_rot, s, smem);
     if (!ok) {
       // copies already in flight must land before the CTA's shared memory goes away
       const unsigned long long t0 = global_timer_ns();
