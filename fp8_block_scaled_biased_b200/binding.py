@@ -11,6 +11,7 @@ current torch CUDA stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -741,8 +742,8 @@ def _raw_stream(dev):
 
 def _call_on(dev, name, *args):
     """Calls the library on the current stream of device `dev`."""
-    fn = getattr(load_library(), name)
-    if dev != torch.cuda.current_device():
+    fn = getattr(_lib or load_library(), name)
+    if dev != torch._C._cuda_getDevice():       # (torch.cuda.current_device looks for its first use each time)
         with torch.cuda.device(dev):
             rc = fn(*args, _raw_stream(dev))
     else:
@@ -781,6 +782,9 @@ def mla_fp8_workspace_bytes(num_heads, num_q):
     return load_library().mla_fp8_workspace(num_heads, num_q)
 
 
+_fp8_workspace = functools.lru_cache(maxsize=256)(mla_fp8_workspace_bytes)
+
+
 def _mla_fp8_attention(name, q, qo_indptr, kv_cache, kv_scale, o, kv_indptr, kv_indices, kv_last_page_lens, sm_scale,
                        logit_cap, lse, workspace):
     dev, batch, pages, page_size, n_idx = _cache_args(kv_cache, kv_scale, kv_indptr, kv_indices, kv_last_page_lens)
@@ -802,9 +806,9 @@ def _mla_fp8_attention(name, q, qo_indptr, kv_cache, kv_scale, o, kv_indptr, kv_
         _ranges(qo_indptr, "qo_indptr", dev, batch)
         ranges, sizes = (qo_indptr.data_ptr(),), (batch, rows, heads)
     if workspace is None:
-        need = mla_fp8_workspace_bytes(heads, rows)
+        need = _fp8_workspace(heads, rows)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(need, dtype=torch.uint8)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse(workspace, torch.uint8, "workspace", dev, "byte")
     _call_on(dev, name, q.data_ptr(), *ranges, kv_cache.data_ptr(), kv_scale.data_ptr(), o.data_ptr(),
