@@ -13,7 +13,7 @@
 //   q / s = hi + lo / 16, s a power of two per (query, head): hi is q / s rounded, and the
 //     rest of an 8-bit significand is exactly a 4-bit one (until lo falls to subnormals,
 //     2^-13 below the row's largest entry). N = 2 x columns.
-//   p = hi + lo / 32 + lo2 / 1024: off by 2^-14 of itself or 2^-22 of the largest weight, so that
+//   p = hi + lo / 32 + lo2 / 1024: off by 2^-12 of itself or 2^-22 of the largest weight, so that
 //     a long faint context beside one dominant token keeps its mass. N = 3 x columns.
 // Products of codes are exact and the MMA sums in fp32. Scales of pages (one per token row,
 // i.e. per TMEM lane) multiply the scores, and the weights before they are split.
@@ -677,7 +677,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
           *reinterpret_cast<uint4*>(smem + lat_half<SM::kHalves>(2 * it + (i >> 4)).slot * kLatHalf +
-                                    ((i >> 3) & 1) * kLatChunk + tid * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                    ((i >> 3) & 1) * kLatChunk + tid * 128 + ((i ^ tid) & 7) * 16) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -997,34 +997,37 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     return;
   }
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < SM::kRots; ++i) mbar_init(&s->rot_empty[i], 1);
-    for (int i = 0; i < SM::kPBufs; ++i) {
-      mbar_init(&s->p_full[i], 4 * kGroups);
-      mbar_init(&s->p_empty[i], 1);
+  if (warp == 0) {                                         // a lane per barrier
+    if (lane < SM::kHalves) {
+      mbar_init(&s->kv_full[lane], SMALL ? 4 : 1);
+      mbar_init(&s->kv_empty[lane], 1);
     }
-    for (int i = 0; i < SM::kHalves; ++i) {
-      mbar_init(&s->kv_full[i], SMALL ? 4 : 1);
-      mbar_init(&s->kv_empty[i], 1);
+    if (lane < SM::kAhead) {
+      mbar_init(&s->rows_full[lane], 1);
+      mbar_init(&s->scale_full[lane], 1);
+      mbar_init(&s->tab_empty[lane], (SMALL ? 4 : 1) + 4 * kGroups);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s->s_full[i], 1);
-      mbar_init(&s->s_empty[i], 4 * kGroups);
-      mbar_init(&s->frag_full[i], 1);
-      mbar_init(&s->frag_empty[i], 2 + 4 * kGroups);
+    if (lane < 2) {
+      mbar_init(&s->rot_empty[lane], 1);
+      mbar_init(&s->s_full[lane], 1);
+      mbar_init(&s->s_empty[lane], 4 * kGroups);
+      mbar_init(&s->frag_full[lane], 1);
+      mbar_init(&s->frag_empty[lane], 2 + 4 * kGroups);
     }
-    for (int i = 0; i < SM::kAhead; ++i) {
-      mbar_init(&s->rows_full[i], 1);
-      mbar_init(&s->scale_full[i], 1);
-      mbar_init(&s->tab_empty[i], (SMALL ? 4 : 1) + 4 * kGroups);
+    if (lane < SM::kPBufs) {
+      mbar_init(&s->p_full[lane], 4 * kGroups);
+      mbar_init(&s->p_empty[lane], 1);
     }
-    mbar_init(&s->q_full, kGroups);
-    s->abort = 0;
+    if (lane == 0) {
+      mbar_init(&s->q_full, kGroups);
+      s->abort = 0;
+    }
     fence_mbar_init();
-    if (!SMALL && a.table.num_indices > 0) {              // (an empty table comes without maps)
+    if (!SMALL && lane == 0 && a.table.num_indices > 0) {  // (an empty table comes without maps)
       prefetch_tensormap(&tm_lat);
       prefetch_tensormap(&tm_rot);
     }
+    __syncwarp();
   }
   if (warp == 2) {
     tmem_alloc(&s->tmem, SM::kTmemCols);

@@ -11,13 +11,12 @@ Attention, from the kernel's arithmetic. With S = sm_scale * max_j <|q|, |k_j|>:
     the argument, itself within 2 S) below 2^-17 (1 + S);
   * so a softmax weight and its normaliser are each off by 2^-17 (1 + S), together
     2^-16 (1 + S) relatively;
-  * a weight times its page's scale becomes three e4m3 codes, hi + lo / 32 + lo2 / 1024. Each
-    term halves a step of four significant bits: 2^-4, then 2^-5 of that (the rest is at most
-    2^-4 of 2^e, times 32 at most 2^(e+1)) and again: 2^-14 relatively, well inside 2^-12. Where
-    lo2 is subnormal (steps of 2^-9 / 1024 = 2^-19) the error is 2^-20 absolutely. The reference
-    is coded as 2^2 (2^4 above 2^14 tokens, 2^6 above 2^16), and nothing that set it is larger
-    than the largest weight times scale, M = max_j p_j s_j: 2^-22 M (2^-24, 2^-26) a token, and
-    with the codes v_j / s_j that it multiplies `faint` = 2^-22 M sum_j |v_j / s_j| in all;
+  * a weight times its page's scale is rounded to fp16's 11 bits, 2^-12 relatively, and becomes
+    three e4m3 codes, hi + lo / 32 + lo2 / 1024: 4, 4 and 3 of the bits, exactly, until lo2 is
+    subnormal (steps of 2^-9 / 1024 = 2^-19): then 2^-20 absolutely. The reference is coded as
+    2^2 (2^4 above 2^14 tokens, 2^6 above 2^16), and nothing that set it is larger than the
+    largest weight times scale, M = max_j p_j s_j: 2^-22 M (2^-24, 2^-26) a token, and with the
+    codes v_j / s_j that it multiplies `faint` = 2^-22 M sum_j |v_j / s_j| in all;
   * fp32 sums of L/32 steps: L * 2^-28;
   * the bf16 output: half a step, 2^-8 relatively.
 |o - o_ref| <= (2^-16 (1 + S) + 2^-12 + 2^-28 L) * sum_j p_j |v_j| + faint + 2^-8 |o_ref| + 1e-30,
