@@ -1138,6 +1138,29 @@ int mla_decode_fwd(const uint16_t* q, const uint16_t* kv_buffer, uint16_t* o, co
 // ------------------------------------------------------------------ the 8-bit latent cache
 namespace {
 
+// Launches a kernel while the work before it in the stream may still run (programmatic dependence): the
+// kernel waits for that work's end itself, once it is set up (64 x 544 tokens: 17.3 to 16.9 us; one
+// sequence of 97: 9.6 to 8.9; one new token for 64 sequences appended: 3.0 to 2.8).
+template <typename... P, typename... A>
+int launch_early(const char* name, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(FP8MOE_ECUDA, "%s: launch failed: %s", name, cudaGetErrorString(e));
+  }
+  return check_launch(name);
+}
+
 // The checks that the cache calls share; fills `t`. Row numbers of the cache and token
 // positions are int32 in the kernels.
 int cache_table(const char* name, const void* kv_cache, const void* kv_scale, const int32_t* kv_indptr,
@@ -1191,8 +1214,8 @@ int mla_kv_append_fp8(const uint16_t* kv_new, int ld_new, const int32_t* append_
   const int rows = std::min(page_size, (num_tokens + batch - 1) / batch);
   const int side = std::max(1, std::min(rows / 8, kAppendMaxRows));
   const unsigned ctas = static_cast<unsigned>(num_tokens / page_size + 2 * batch);
-  mla_kv_append_kernel<<<ctas, (side * kLatVec + 31) / 32 * 32, 0, static_cast<cudaStream_t>(stream)>>>(a, side);
-  return check_launch(name);
+  return launch_early(name, mla_kv_append_kernel, dim3(ctas), (side * kLatVec + 31) / 32 * 32, 0,
+                      static_cast<cudaStream_t>(stream), a, side);
 }
 
 int mla_kv_gather_fp8(const uint8_t* kv_cache, const float* kv_scale, const int32_t* kv_indptr,
@@ -1219,9 +1242,8 @@ int mla_kv_gather_fp8(const uint8_t* kv_cache, const float* kv_scale, const int3
   a.ld = ld_out;
   a.T = num_rows;
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ld_out % 16 == 0;
-  mla_kv_gather_kernel<<<(num_rows + kGatherRows - 1) / kGatherRows, kGatherThreads, 0,
-                         static_cast<cudaStream_t>(stream)>>>(a);
-  return check_launch(name);
+  return launch_early(name, mla_kv_gather_kernel, dim3((num_rows + kGatherRows - 1) / kGatherRows), kGatherThreads, 0,
+                      static_cast<cudaStream_t>(stream), a);
 }
 
 // Workspace of the attention calls: the joining kernel's jobs, then the parts' references and
@@ -1243,26 +1265,12 @@ static int lat_launch(const char* name, LatAttnArgs a, const CUtensorMap& lat, c
   a.merge = reinterpret_cast<int4*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + lat_parts_offset());
   a.part_o = reinterpret_cast<float*>(ws + lat_acc_offset(HG));
-  mla_fp8_kernel<HG, SMALL><<<ctas, kLatThreads<HG, SMALL>, LatSmem<HG>::kBytes, st>>>(lat, rot, a);
-  if (int rc = check_launch(name)) return rc;
+  if (int rc = launch_early(name, mla_fp8_kernel<HG, SMALL>, dim3(ctas), kLatThreads<HG, SMALL>, LatSmem<HG>::kBytes, st,
+                            lat, rot, a))
+    return rc;
   // a table of one tile cuts nothing
   if (static_cast<long long>(a.table.num_indices) * a.table.page_size <= kLatTile) return FP8MOE_OK;
-  // launched while the attention kernel runs (programmatic dependence): it waits for its end itself
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, HG);
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_fp8_join_kernel<HG>, a);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(FP8MOE_ECUDA, "%s: launch failed: %s", name, cudaGetErrorString(e));
-  }
-  return check_launch(name);
+  return launch_early(name, mla_fp8_join_kernel<HG>, dim3(ctas, HG), 128, 0, st, a);
 }
 
 extern "C" {

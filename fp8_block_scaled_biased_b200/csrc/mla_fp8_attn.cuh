@@ -991,6 +991,7 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   constexpr int kGroups = SM::kGroups;
   if (smem + SM::kUsed > smem_raw + SM::kBytes) {          // (an unaligned start of shared memory)
     if (threadIdx.x == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       raise_device_error(FP8MOE_DEVERR_TIMEOUT);
       a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
@@ -1033,6 +1034,9 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     tmem_alloc(&s->tmem, SM::kTmemCols);
     tmem_relinquish();
   }
+  // Launched while the work before it in the stream may still run: nothing above reads or writes what
+  // that work does.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // the work list's length, and the sequence that this CTA's share begins in: a run of
   // sequences per thread, then a scan over the threads
   const int per = (a.table.B + kThreads - 1) / kThreads;

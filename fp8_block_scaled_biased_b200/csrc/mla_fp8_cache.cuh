@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
   __shared__ uint32_t warp_max[16];
   const int tid = threadIdx.x;
   const int ps = a.table.page_size;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the work before this in the stream is done
   const int count = count_sequences(
       a.table.B, [&](int b) { return __ldg(a.append_indptr + b) / ps + 2ll * b <= blockIdx.x; });
   if (count == 0) return;
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const Gat
   __shared__ float row_scale[kGatherRows];
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * kGatherRows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the work before this in the stream is done
   const int before = count_sequences(a.table.B, [&](int b) { return __ldg(a.out_indptr + b) <= t0; });
   if (tid < kGatherRows) {
     const int t = t0 + tid;

@@ -585,6 +585,56 @@ def test_captured_step_replays_on_new_contents():
         _check(b, qs, torch.arange(3), o, lse)
 
 
+def test_calls_wait_for_the_work_before_them():
+    """Kernels are launched early and wait by themselves: for copies, fills, another stream's work and
+    each other, captured and not."""
+    b = Batch([300, 40, 129, 700], 64, seed=53).device()
+    H, lens = 16, b.lens
+    q, x = b.q(4, H).to(DEV), torch.randn(4, 576, generator=b.g).to(torch.bfloat16).to(DEV)
+    ip, full = _indptr([1] * 4).to(DEV), _indptr(lens).to(DEV)
+    codes, scales = b.dc.clone(), b.ds.clone()
+    q_in, x_in = torch.zeros_like(q), torch.zeros_like(x)
+    big = torch.zeros(32 << 20, device=DEV)
+    o = torch.zeros(4, H, 512, dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros(sum(lens), 576, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step():
+        b.dc.copy_(codes)
+        b.ds.copy_(scales)
+        big.zero_()
+        x_in.copy_(x)
+        B.mla_kv_append_fp8(x_in, ip, b.dc, b.ds, *b.dt)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            big.add_(1.0)
+            q_in.copy_(q)
+        here.wait_stream(side)
+        B.mla_decode_fp8_fwd(q_in, b.dc, b.ds, o, *b.dt)
+        B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, full, out)
+        x_in.zero_()
+        q_in.zero_()
+
+    step()
+    torch.cuda.synchronize()
+    want_codes, want_scales = M8.append(x.cpu(), _indptr([1] * 4), b.codes, b.scales, *b.table)
+    assert torch.equal(_codes(b.dc), want_codes) and torch.equal(b.ds.cpu(), want_scales)
+    first = o.clone()
+    b.codes, b.scales = want_codes, want_scales
+    _check(b, q.cpu(), torch.arange(5), o, _decode(b, q.cpu())[1])
+    want = M8.gather(want_codes, want_scales, b.indptr, b.indices, _indptr(lens), torch.zeros_like(out).cpu())
+    assert torch.equal(out.cpu(), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for run in [step] * 10 + [g.replay] * 10:
+        o.fill_(math.nan)
+        out.zero_()
+        run()
+        assert torch.equal(o, first) and torch.equal(out.cpu(), want)
+
+
 def test_two_captured_graphs_share_a_workspace():
     b = Batch([700, 30, 300], 64, seed=52).device()
     ws = torch.empty(B.mla_fp8_workspace_bytes(128, 3), dtype=torch.uint8, device=DEV)
