@@ -10,7 +10,8 @@
  * end follow the same page's TP8 run and custom all-reduce ("Performance
  * Reproduction for AITER-Optimized in SGLang", "Other Operators") and asm_moe's
  * expert_mask. The MLA decode entry point at the very end follows the same page's
- * section "Attention Mechanisms" ("MLA For Decode").
+ * section "Attention Mechanisms" ("MLA For Decode"); the 8-bit latent cache's entry
+ * points after it hold that section's paged KV buffer in FP8.
  *
  * Conventions for every entry point:
  *   - Tensor pointers are DEVICE pointers owned by the caller; the library never
