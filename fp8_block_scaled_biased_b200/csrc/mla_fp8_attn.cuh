@@ -28,10 +28,11 @@
 //               then the accumulators in TMEM are rescaled.
 //
 // Work list: the tiles of all (sequence, column group) pairs in one row, cut into equal
-// shares; a share may begin and end inside a pair. Pairs cut in parts leave unnormalised
-// fp32 partials (two per CTA at most) that a second kernel joins in order. Sequences with
-// several column groups give them to a gang of G neighbouring CTAs that walk the same tiles
-// at the same time, so that the rows come from HBM once and from L2 G - 1 times.
+// shares; a share may begin and end inside a pair. (Few and short sequences: one each.) Pairs
+// cut in parts leave unnormalised fp32 partials (two per CTA at most) that a second kernel
+// joins in order. Sequences with several column groups give them to a gang of G neighbouring
+// CTAs that walk the same tiles at the same time, so that the rows come from HBM once and from
+// L2 G - 1 times.
 #pragma once
 
 #include "gemm_sm100.cuh"
@@ -116,6 +117,7 @@ struct LatSmem {
     uint64_t s_full[2], s_empty[2], p_full[kPBufs], p_empty[kPBufs];
     uint64_t frag_full[2], frag_empty[2], q_full;
     long long scan[24];
+    int scan_most[24];
     long long start_off;          // position of the first sequence of this CTA's share,
     int start_b;                  // the sequence, and its shape
     LatShape start;
@@ -1052,20 +1054,41 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
     const long long up = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += up;
   }
-  if (lane == 31) s->scan[warp] = incl;
+  // tiles of the longest sequence, if none has more than one column group
+  const int most_here = static_cast<int>(
+      __reduce_max_sync(0xffffffffu, per > 1 || sh.groups > 1 ? 0x7fffffffu : static_cast<unsigned>(sh.tiles)));
+  if (lane == 31) {
+    s->scan[warp] = incl;
+    s->scan_most[warp] = most_here;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   long long before = incl - mine, total = 0;
+  int most = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s->scan[w];
     total += s->scan[w];
+    most = max(most, s->scan_most[w]);
   }
   const int gang_id = blockIdx.x >> a.gang_log, rank = blockIdx.x - (gang_id << a.gang_log);
-  const int ngangs = static_cast<int>(min(static_cast<long long>(gridDim.x >> a.gang_log), total));
-  const bool works = gang_id < ngangs;
-  const long long p0 = works ? lat_div(total * gang_id, ngangs) : 0;
-  if (works && p0 >= before && p0 < before + mine) {
+  const int gangs = static_cast<int>(gridDim.x >> a.gang_log);
+  // A sequence per gang, whole, where they are few and the longest has little more than an equal share:
+  // a tile more costs less than a second fragment and joining. On 16 columns 2.9 tiles more gained 0.9
+  // us (64 x 544 tokens: 15.8 instead of 16.8), 3.8 lost 2 (8 x 400); on 32, 2.9 gained 1.6 (two
+  // queries each of 64 x 544: 20.7 instead of 22.3) and 2.5 four (30 x 700 on 128 heads: 25 instead of 29).
+  constexpr int kQuarters = HG == 16 ? 13 : 15;
+  const bool whole = a.table.B <= gangs && (4ll * most - kQuarters) * gangs <= 4 * total;
+  const int ngangs = static_cast<int>(min(static_cast<long long>(gangs), total));
+  const long long p0 = lat_div(total * gang_id, max(ngangs, 1));
+  const bool works = gang_id < (whole ? a.table.B : ngangs);
+  if (whole) {
+    if (static_cast<int>(threadIdx.x) == gang_id) {          // (without a sequence: an empty share)
+      s->start_b = gang_id;
+      s->start_off = before;
+      s->start = sh;
+    }
+  } else if (works && p0 >= before && p0 < before + mine) {
     long long off = before;
     for (int b = b0; b < b1; ++b) {
       if (per > 1) sh = lat_shape(a, b, HG);
@@ -1094,8 +1117,11 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   } else if (warp == 1) {
     ok = lat_score_role<HG>(s, smem, tmem);
   } else if (warp == 3) {
-    LatSchedule<HG> schedule{s->start, s->start_b,  s->start_off, p0, p0, lat_div(total * (gang_id + 1), ngangs), total,
-                             ngangs,   gang_id,     rank,         make_int4(0, 0, 0, 0)};
+    const long long from = whole ? s->start_off : p0;
+    const long long to = whole ? from + static_cast<long long>(s->start.groups) * s->start.tiles
+                               : lat_div(total * (gang_id + 1), ngangs);
+    LatSchedule<HG> schedule{s->start, s->start_b, s->start_off, from, from, to, total, ngangs, gang_id, rank,
+                             make_int4(0, 0, 0, 0)};
     ok = lat_table_role<HG, SMALL>(a, s, schedule);
     if (!ok && lane == 0) a.merge[blockIdx.x] = make_int4(0, 0, 0, 0);   // the joining kernel must not find old words
   } else if constexpr (!SMALL) {

@@ -234,6 +234,17 @@ def test_decode_ragged_lengths_heads_and_pages(ps, H):
     _check(b, q, torch.arange(9), o, lse)
 
 
+@pytest.mark.parametrize("ps", [3, 64])
+@pytest.mark.parametrize("H", [2, 16, 40, 128])
+def test_decode_short_beside_long(ps, H):
+    """Sequences cut into parts beside whole ones, and alone in a share beside empty ones."""
+    for lens in ([0, 1, 900, 128, 129, 2, 640, 0], [500, 0, 0, 505], [130] * 30 + [0] * 6, [200] * 40):
+        b = Batch(lens, ps, seed=H + ps + len(lens)).device()
+        q = b.q(len(lens), H)
+        o, lse = _decode(b, q)
+        _check(b, q, torch.arange(len(lens) + 1), o, lse)
+
+
 def test_decode_long_and_many():
     b = Batch([3000, 5, 1711], 64, seed=1).device()
     q = b.q(3, 16)
