@@ -1310,8 +1310,8 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
   a.logit_cap = logit_cap;
   a.cache = kv_cache;
   // Rows that a page holds together come by TMA boxes: the largest power of two in page_size. Boxes of 8
-  // rows still keep up (64 x 8192 tokens on 16 heads: 73 us, as copied by four warps; 24 x 4096 on 128
-  // heads: 59 against 76, because the copying warps leave threads for 16 columns only); below that the
+  // rows still win (64 x 8192 tokens on 16 heads: 70 us, copied by four warps 71; 24 x 4096 on 128 heads:
+  // 55 against 71, because beside the copying warps there is room for 16 columns only); below that the
   // rows of a box no longer fill the pattern that the MMAs read, and the four warps copy.
   a.run = std::min(kLatTile, page_size & -page_size);
   const bool small = a.run < 8;

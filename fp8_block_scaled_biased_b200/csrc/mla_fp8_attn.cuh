@@ -92,9 +92,9 @@ struct LatSmem {
   static constexpr int kQRows = 2 * HG, kPRows = 3 * HG;
   static constexpr int kQBytes = kQRows * kLatDk;
   static constexpr int kPBytes = kPRows * kLatTile;
-  // What shared memory holds: 2.5 tiles in halves (with 2, 64 x 8192 tokens on 16 heads took 78 us
-  // instead of 73), the rotary bytes of two, the queries' terms, and the weights of two tiles, or of
-  // one beside 32 columns' queries.
+  // What shared memory holds: 2.5 tiles in halves (2 whole tiles cost 64 x 8192 tokens on 16 heads 7%),
+  // the rotary bytes of two, the queries' terms, and the weights of two tiles, or of one beside 32
+  // columns' queries.
   static constexpr int kHalves = 5, kRots = 2, kPBufs = HG == 16 ? 2 : 1;
   static constexpr int kAhead = HG == 16 ? 4 : 2;          // tiles whose page-table entries are fetched ahead
   static constexpr int kOffRot = kHalves * kLatHalf;
@@ -698,8 +698,9 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
 // ---------------------------------------------------------------- MMA warps
 // Scores and P V are issued by a warp each, so that one's waits pass while the other's MMAs run: with
 // both in one warp a tile of 32 columns took 3170 cycles, of which its MMAs 1770 and what lay between
-// them 670 (chunks of 500 queries on 16 heads: 182 us instead of 162). All lanes run the loops and one elected lane issues, so that descriptors stay in
-// uniform registers: 44 and 48 cycles per MMA (16 columns), 70 from a divergent branch.
+// them 670 (chunks of 500 queries on 16 heads: 182 us instead of 162). All lanes run the loops and one
+// elected lane issues, so that descriptors stay in uniform registers: 44 and 48 cycles per MMA (16
+// columns), 70 from a divergent branch.
 template <int HG>
 __device__ __forceinline__ bool lat_score_role(typename LatSmem<HG>::Info* s, uint8_t* smem, uint32_t tmem_any) {
   using SM = LatSmem<HG>;
@@ -906,9 +907,11 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
 }
 
 // Four warps, smaller pages: 16-byte asynchronous copies into the places (and the swizzle) that the
-// boxes would use. A tile of single rows took 4500 cycles as TMA gathers from four warps, 40 boxes of
-// 16 rows 4400; this takes 3200 or less, about what HBM needs. A warp copies 32 rows; each of its
-// instructions 64 bytes of 8 rows.
+// boxes would use. A tile of single rows took 4500 cycles as TMA gathers from four warps; this takes
+// 3200 or less, about what HBM needs (64 x 8192 tokens on 16 heads, a page each: 84 us; pages of 64,
+// by TMA: 66). A warp copies 32 rows; each of its instructions 64 bytes of 8 rows. With 32 columns'
+// queries there is no room for single rows' places: more columns take several CTAs (24 x 4096 tokens on
+// 128 heads: 77 us against 49).
 template <int HG>
 __device__ __forceinline__ bool lat_copy_role(const LatAttnArgs& a, const uint8_t* cache, typename LatSmem<HG>::Info* s,
                                               uint8_t* smem) {
