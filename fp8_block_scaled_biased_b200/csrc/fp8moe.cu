@@ -120,6 +120,8 @@ int device_setup(int* sm_count) {
     if (r == cudaSuccess)
       r = cudaFuncSetAttribute(mla_fp8_kernel<32, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<32>::kBytes);
     if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(mla_fp8_kernel<32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatSmem<32>::kBytes);
+    if (r == cudaSuccess)
       r = cudaFuncSetAttribute(sort_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(sort_scatter_smem(kSortMaxExperts)));
     if (r == cudaSuccess)
@@ -1310,9 +1312,8 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
   a.logit_cap = logit_cap;
   a.cache = kv_cache;
   // Rows that a page holds together come by TMA boxes: the largest power of two in page_size. Boxes of 8
-  // rows still win (64 x 8192 tokens on 16 heads: 70 us, copied by four warps 71; 24 x 4096 on 128 heads:
-  // 55 against 71, because beside the copying warps there is room for 16 columns only); below that the
-  // rows of a box no longer fill the pattern that the MMAs read, and the four warps copy.
+  // rows still win (64 x 8192 tokens on 16 heads: 70 us, copied by four warps 71); below that the rows of a
+  // box no longer fill the pattern that the MMAs read, and four warps copy.
   a.run = std::min(kLatTile, page_size & -page_size);
   const bool small = a.run < 8;
   CUtensorMap lat, rot;
@@ -1327,13 +1328,20 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
                              CU_TENSOR_MAP_SWIZZLE_64B))
       return rc;
   }
-  // 16 columns per CTA where a sequence has no more, else 32; a gang of CTAs for its column groups
+  // 16 columns per CTA where a sequence has no more, and for short work lists, whose time is the set-up
+  // and the change of fragments (shorter with 16): below 7.5 tiles of 16 columns per SM. At 4.1 tiles (64 x
+  // 600 tokens, two queries on 16 heads) 19.5 us with 16, 23.6 with 32; at 6.8 (64 x 1000, 32 heads) 24.6
+  // and 29.2; at 8.1 (64 x 600, four queries) 30.2 and 24.6; at 8.9 (30 x 700, 128 heads) 30.7 and 25.1; at 41
+  // (24 x 4096, 128 heads, a page per token) 78 and 61. A gang of CTAs for a sequence's column groups.
   const long long cols = (static_cast<long long>(num_q) * num_heads + batch - 1) / batch;
-  const int hg = cols <= 16 || small ? 16 : 32;
+  const long long tiles = (static_cast<long long>(num_indices) * page_size + kLatTile - 1) / kLatTile * ((cols + 15) / 16);
+  const int hg = cols <= 16 || 2 * tiles < 15ll * sms ? 16 : 32;
   a.gang_log = cols > 3 * hg ? 2 : cols > hg ? 1 : 0;
   const int ctas = std::max(1, std::min(sms, kLatMaxCtas) >> a.gang_log) << a.gang_log;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (small) return lat_launch<16, true>(name, a, lat, rot, ctas, workspace, st);
+  if (small)
+    return hg == 16 ? lat_launch<16, true>(name, a, lat, rot, ctas, workspace, st)
+                    : lat_launch<32, true>(name, a, lat, rot, ctas, workspace, st);
   return hg == 16 ? lat_launch<16, false>(name, a, lat, rot, ctas, workspace, st)
                   : lat_launch<32, false>(name, a, lat, rot, ctas, workspace, st);
 }

@@ -108,19 +108,23 @@ struct LatSmem {
   struct Info {
     LatFragment frag[2];
     // per tile: the tokens' rows (or only those that begin a box), -1 for none; the tokens' scales
-    int rows[kAhead][HG == 16 ? kLatTile : 32];
+    union {
+      int rows[kAhead][kLatTile];
+      struct {                    // at the start only: the table warp reads it before it writes rows
+        long long scan[24];
+        int scan_most[24];
+        long long start_off;      // position of the first sequence of this CTA's share,
+        int start_b;              // the sequence, and its shape
+        LatShape start;
+      };
+    };
     float scale[kAhead][kLatTile];
     int live[kAhead];             // rows to be loaded; -1: the end of the list
     uint64_t rows_full[kAhead], scale_full[kAhead], tab_empty[kAhead];
-    float red[kGroups][4][8], inv[kGroups][8], qfac[2][kGroups][8];
+    float red[kGroups][4][8], qfac[kGroups][8];   // (of red, row 0 then holds reciprocals of the sums)
     uint64_t kv_full[kHalves], kv_empty[kHalves], rot_empty[kRots];
     uint64_t s_full[2], s_empty[2], p_full[kPBufs], p_empty[kPBufs];
     uint64_t frag_full[2], frag_empty[2], q_full;
-    long long scan[24];
-    int scan_most[24];
-    long long start_off;          // position of the first sequence of this CTA's share,
-    int start_b;                  // the sequence, and its shape
-    LatShape start;
     uint32_t tmem;
     int abort;
   };
@@ -439,7 +443,6 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
   int fslot = 0;
   uint32_t fphase = 0;
   int it = 0;                                              // tiles so far: buffers and phases follow it
-  int nfrag = 0;
   LatFragment f;
   bool ok;
   // The next fragment, its queries split and handed to the score MMAs. The MMAs of the fragment before
@@ -455,8 +458,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     LatQueries<HG> queries;
     queries.load(a, to, group, tid);
     const float qscale = queries.store(smem + SM::kOffQ, group, tid);
-    if ((tid & 15) == 0) s->qfac[nfrag & 1][group][tid >> 4] = qscale * (a.sm_scale * (capped ? 1.0f : kLog2e));
-    ++nfrag;
+    if ((tid & 15) == 0) s->qfac[group][tid >> 4] = qscale * (a.sm_scale * (capped ? 1.0f : kLog2e));
     fence_proxy_async_smem();
     group_sync(bar_id);
     if (tid == 0) mbar_arrive(&s->q_full);
@@ -496,12 +498,12 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
           if (f.slot >= 0) a.part_ml[part0 + tid] = make_float2(m, l);
           else if (a.lse) a.lse[row0 + tid] = l == 0.0f ? -INFINITY : (log2f(l) - m) * kLn2;
         }
-        s->inv[group][tid] = l == 0.0f ? 0.0f : 1.0f / l;
+        s->red[group][0][tid] = l == 0.0f ? 0.0f : 1.0f / l;
       }
       group_sync(bar_id);
       if (f.slot < 0) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) sum[c] = s->inv[group][c];
+        for (int c = 0; c < 8; ++c) sum[c] = s->red[group][0][c];
         // neighbouring lanes share the work: the even one stores both values of columns 0 .. 3, the odd one
         // those of 4 .. 7 (half as many, twice as wide stores)
         const bool odd = lane & 1;
@@ -542,7 +544,7 @@ __device__ __forceinline__ bool lat_softmax_role(const LatAttnArgs& a, typename 
     float fac[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      fac[c] = s->qfac[(nfrag - 1) & 1][group][c];
+      fac[c] = s->qfac[group][c];
       nref[c] = kLatNoRef;
       sum[c] = 0.0f;
     }
@@ -909,9 +911,7 @@ __device__ __forceinline__ bool lat_load_role(const LatAttnArgs& a, const CUtens
 // Four warps, smaller pages: 16-byte asynchronous copies into the places (and the swizzle) that the
 // boxes would use. A tile of single rows took 4500 cycles as TMA gathers from four warps; this takes
 // 3200 or less, about what HBM needs (64 x 8192 tokens on 16 heads, a page each: 84 us; pages of 64,
-// by TMA: 66). A warp copies 32 rows; each of its instructions 64 bytes of 8 rows. With 32 columns'
-// queries there is no room for single rows' places: more columns take several CTAs (24 x 4096 tokens on
-// 128 heads: 77 us against 49).
+// by TMA: 66). A warp copies 32 rows; each of its instructions 64 bytes of 8 rows.
 template <int HG>
 __device__ __forceinline__ bool lat_copy_role(const LatAttnArgs& a, const uint8_t* cache, typename LatSmem<HG>::Info* s,
                                               uint8_t* smem) {

@@ -69,10 +69,15 @@ class Batch:
     def table(self):
         return self.indptr, self.indices, self.last
 
-    def device(self):
+    def device(self, wide=False):
+        """wide: a table with room for 144K tokens, as a serving program keeps it. The call then
+        takes a long work list's 32 columns per CTA where a sequence has more than 16."""
         self.dc = self.codes.view(torch.float8_e4m3fn).to(DEV)
         self.ds = self.scales.to(DEV)
-        self.dt = tuple(t.to(DEV) for t in self.table)
+        indptr, indices, last = self.table
+        if wide:
+            indices = torch.cat([indices, torch.full((-(-144 * 1024 // self.ps),), -1, dtype=torch.int32)])
+        self.dt = (indptr.to(DEV), indices.to(DEV), last.to(DEV))
         return self
 
     def q(self, rows, H, std=1.0):
@@ -225,21 +230,23 @@ def test_gather_matches_the_oracle_and_leaves_other_rows(ps):
 
 
 # ---------------------------------------------------------------- decode
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("ps", [1, 7, 64, 200])
 @pytest.mark.parametrize("H", [1, 8, 16, 24, 128])
-def test_decode_ragged_lengths_heads_and_pages(ps, H):
-    b = Batch([0, 1, 127, 128, 129, 2, 300, 64], ps, seed=H + ps).device()
+def test_decode_ragged_lengths_heads_and_pages(ps, H, wide):
+    b = Batch([0, 1, 127, 128, 129, 2, 300, 64], ps, seed=H + ps).device(wide)
     q = b.q(8, H)
     o, lse = _decode(b, q)
     _check(b, q, torch.arange(9), o, lse)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("ps", [3, 64])
 @pytest.mark.parametrize("H", [2, 16, 40, 128])
-def test_decode_short_beside_long(ps, H):
+def test_decode_short_beside_long(ps, H, wide):
     """Sequences cut into parts beside whole ones, and alone in a share beside empty ones."""
     for lens in ([0, 1, 900, 128, 129, 2, 640, 0], [500, 0, 0, 505], [130] * 30 + [0] * 6, [200] * 40):
-        b = Batch(lens, ps, seed=H + ps + len(lens)).device()
+        b = Batch(lens, ps, seed=H + ps + len(lens)).device(wide)
         q = b.q(len(lens), H)
         o, lse = _decode(b, q)
         _check(b, q, torch.arange(len(lens) + 1), o, lse)
@@ -375,7 +382,7 @@ def test_decode_and_gather_of_a_shared_prefix():
 
 @pytest.mark.parametrize("H, bad", [(8, 0), (5, 0), (16, 3), (24, 17)])
 def test_decode_nan_in_one_head_leaves_the_others(H, bad):
-    b = Batch([130, 300], 16, seed=13).device()
+    b = Batch([130, 300], 16, seed=13).device(wide=True)
     q = b.q(2, H)
     clean = q.clone()
     q[:, bad, 40] = math.nan
@@ -388,7 +395,7 @@ def test_decode_nan_in_one_head_leaves_the_others(H, bad):
 
 @pytest.mark.parametrize("H", [1, 8, 16, 32])
 def test_extend_a_nan_query_leaves_the_other_queries(H):
-    b = Batch([200, 40], 64, seed=14).device()
+    b = Batch([200, 40], 64, seed=14).device(wide=H != 16)
     qo = _indptr([6, 3])
     q = b.q(9, H)
     clean = q.clone()
@@ -428,10 +435,11 @@ def test_decode_scales_at_the_ends_of_their_range():
 
 
 # ---------------------------------------------------------------- extend
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("ps", [2, 8, 16, 32, 96, 128, 256])
 @pytest.mark.parametrize("H", [5, 48])
-def test_extend_by_page_size(ps, H):
-    b = Batch([129, 1, 400, 128, 257], ps, seed=ps + H).device()
+def test_extend_by_page_size(ps, H, wide):
+    b = Batch([129, 1, 400, 128, 257], ps, seed=ps + H).device(wide)
     new = [9, 1, 4, 0, 13]
     qo = _indptr(new)
     q = b.q(sum(new), H)
@@ -439,13 +447,14 @@ def test_extend_by_page_size(ps, H):
     _check(b, q, qo, o, lse)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("H", [3, 16, 40, 128])
 @pytest.mark.parametrize("ps", [1, 48])
-def test_extend_ragged(ps, H):
+def test_extend_ragged(ps, H, wide):
     lens, new = [5, 0, 140, 260, 33, 128, 9], [5, 0, 2, 37, 0, 128, 1]
     if H == 128:
         new = [5, 0, 2, 7, 0, 20, 1]
-    b = Batch(lens, ps, seed=ps + H).device()
+    b = Batch(lens, ps, seed=ps + H).device(wide)
     qo = _indptr(new)
     q = b.q(sum(new) + 3, H)                               # three rows behind the last sequence
     o, lse = _extend(b, q, qo, fill=3.0)
