@@ -1077,9 +1077,9 @@ mla_fp8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant
   const int gang_id = blockIdx.x >> a.gang_log, rank = blockIdx.x - (gang_id << a.gang_log);
   const int gangs = static_cast<int>(gridDim.x >> a.gang_log);
   // A sequence per gang, whole, where they are few and the longest has little more than an equal share:
-  // a tile more costs less than a second fragment and joining. On 16 columns 2.9 tiles more gained 0.9
-  // us (64 x 544 tokens: 15.8 instead of 16.8), 3.8 lost 2 (8 x 400); on 32, 2.9 gained 1.6 (two
-  // queries each of 64 x 544: 20.7 instead of 22.3) and 2.5 four (30 x 700 on 128 heads: 25 instead of 29).
+  // a tile more costs less than a second fragment and joining. On 16 columns 2.9 tiles more gained 1.0
+  // us (64 x 544 tokens: 15.8 instead of 16.8), 3.8 lost 2 (8 x 400); on 32, 2.5 gained four (30 x 700 on
+  // 128 heads: 25 instead of 29).
   constexpr int kQuarters = HG == 16 ? 13 : 15;
   const bool whole = a.table.B <= gangs && (4ll * most - kQuarters) * gangs <= 4 * total;
   const int ngangs = static_cast<int>(min(static_cast<long long>(gangs), total));
