@@ -95,18 +95,19 @@ __device__ __forceinline__ uint32_t finite_magnitudes(uint32_t v) {
   return v & ~__vcmpgeu2(v, 0x7f807f80u);
 }
 
-// Sequences whose entry of `indptr` plus b * slack is at most x (both grow with b): all threads of the
-// CTA count together.
+// Sequences that start by some place, which grows with b: all threads of the CTA search together, one
+// round where there are no more sequences than threads, two or three for the most there can be.
 template <typename F>
 __device__ __forceinline__ int count_sequences(int B, F&& starts_by) {
-  int count = 0;
-  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    const int n = __syncthreads_count(b < B && starts_by(b));
-    count += n;
-    if (n < static_cast<int>(blockDim.x)) break;
+  const int threads = static_cast<int>(blockDim.x);
+  int lo = 0, hi = B;                                        // the count lies between them
+  while (lo < hi) {
+    const int step = hi - lo <= threads ? 1 : (hi - lo + threads - 1) / threads;
+    const int at = lo + (static_cast<int>(threadIdx.x) + 1) * step - 1;     // the last of this thread's share
+    lo += __syncthreads_count(at < hi && starts_by(at)) * step;
+    hi = min(hi, lo + step - 1);
   }
-  return count;
+  return hi;
 }
 
 // One CTA per (sequence, page written): the largest magnitude of the page's new rows, the page's

@@ -194,6 +194,38 @@ def test_append_large_page_and_many_sequences():
     _append_and_check(b, torch.randn(sum(counts), 576, generator=b.g).to(torch.bfloat16), counts)
 
 
+@pytest.mark.parametrize("B_", [97, 513, 20000])
+def test_append_and_gather_of_many_short_sequences(B_):
+    """More sequences than a CTA has threads, some of them empty or without new tokens."""
+    g = torch.Generator().manual_seed(B_)
+    lens = torch.randint(0, 4, (B_,), generator=g)
+    new = torch.minimum(torch.randint(0, 3, (B_,), generator=g), lens)
+    pages = (lens + 1) // 2
+    n = int(pages.sum())
+    indptr = _indptr(pages.tolist())
+    last = torch.where(lens > 0, lens - (pages - 1) * 2, 0).to(torch.int32)
+    table = (indptr.to(DEV), torch.randperm(n, generator=g).to(torch.int32).to(DEV), last.to(DEV))
+    cache = torch.zeros(n, 2, 1, 576, dtype=torch.float8_e4m3fn, device=DEV)
+    scale = torch.zeros(n, 1, device=DEV)
+    want = torch.zeros(int(lens.sum()), 576, dtype=torch.bfloat16)
+    full = _indptr(lens.tolist())
+    for counts, offset in ((lens - new, torch.zeros_like(lens)), (new, lens - new)):
+        # small integers: exact in the cache whatever the page's scale
+        x = torch.randint(-7, 8, (int(counts.sum()), 576), generator=g).to(torch.bfloat16)
+        done = offset + counts
+        used = (done + 1) // 2
+        at = torch.cat([torch.arange(int(u)) + int(i) for u, i in zip(used, indptr[:-1])]) if int(used.sum()) else torch.zeros(0)
+        now = (_indptr(used.tolist()).to(DEV), table[1][at.long().to(DEV)].contiguous(),
+               torch.where(done > 0, done - (used - 1) * 2, 0).to(torch.int32).to(DEV))
+        B.mla_kv_append_fp8(x.to(DEV), _indptr(counts.tolist()).to(DEV), cache, scale, *now)
+        seq = torch.repeat_interleave(torch.arange(B_), counts)
+        place = torch.arange(len(x)) - torch.repeat_interleave(_indptr(counts.tolist())[:-1].long(), counts)
+        want[full[:-1].long()[seq] + offset[seq] + place] = x
+    out = torch.full((len(want) + 2, 576), 9.0, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_gather_fp8(cache, scale, *table, full.to(DEV), out)
+    assert torch.equal(out[:-2].cpu(), want) and (out[-2:] == 9).all()
+
+
 def test_append_and_gather_of_nothing():
     b = Batch([3, 0], 4).device()
     before = _codes(b.dc)
