@@ -258,8 +258,8 @@ __device__ __noinline__ LatShape lat_shape(const LatAttnArgs& a, int b, int HG) 
   LatShape s{};
   int qlo = b, qhi = b + 1;
   if (a.qo_indptr) {
-    qlo = __ldg(a.qo_indptr + b);
-    qhi = __ldg(a.qo_indptr + b + 1);
+    qlo = a.qo_indptr[b];
+    qhi = a.qo_indptr[b + 1];
   }
   const bool table = sequence_extent(a.table, b, s.first, s.len);
   if (qlo < 0 || qhi < qlo || qhi > a.num_q) {
@@ -393,7 +393,7 @@ struct LatQueries {
     const uint2* src =
         reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(f.row0) + (c < f.cols ? c : 0)) * kLatDk) + (tid & 15);
 #pragma unroll
-    for (int j = 0; j < 9; ++j) x[j] = __ldg(src + j * 16);
+    for (int j = 0; j < 9; ++j) x[j] = src[j * 16];
   }
 
   // Splits the entries into their two terms and stores them as the score MMAs' B operand: core
@@ -846,7 +846,7 @@ __device__ __forceinline__ bool lat_table_role(const LatAttnArgs& a, typename La
       if (lane == 0) mbar_arrive(&s->rows_full[slot]);
       float sc[4];
 #pragma unroll
-      for (int i = 0; i < (SMALL ? 4 : 1); ++i) sc[i] = page[i] < 0 ? 0.0f : __ldg(a.scale + page[i]);
+      for (int i = 0; i < (SMALL ? 4 : 1); ++i) sc[i] = page[i] < 0 ? 0.0f : a.scale[page[i]];
       if constexpr (!SMALL) sc[0] = sc[1] = sc[2] = sc[3] = __shfl_sync(0xffffffffu, sc[0], 4 * lane / run);
       *reinterpret_cast<float4*>(&s->scale[slot][4 * lane]) = make_float4(sc[0], sc[1], sc[2], sc[3]);
       __syncwarp();

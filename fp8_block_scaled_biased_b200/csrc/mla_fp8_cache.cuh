@@ -20,6 +20,11 @@ constexpr int kLatDk = 576;                  // entries of a cache row (512 late
 constexpr int kLatVec = kLatDk / 8;          // 16-byte pieces of a bf16 row
 constexpr int kScaleMinExp = -110;           // keeps 1 / scale and products with it normal fp32
 
+// These kernels and the attention's are launched while the work before them may still write what they read
+// (a page's scale, say, that the append before a decode has just raised), and wait for its end themselves.
+// A kernel's whole life counts for the read-only path (__ldg, ld.global.nc), the time before that wait too,
+// and a line that an SM read over it earlier may be an old one. So all their loads are ordinary ones.
+
 // The page table of a batch, and the buffer it points into.
 struct PageTable {
   const int32_t* indptr;         // [B + 1]
@@ -31,7 +36,7 @@ struct PageTable {
 // First page-table entry and token count of sequence b; false (and flagged) if the table's
 // entries for it are out of range. An empty sequence is a valid one of 0 tokens.
 __device__ __forceinline__ bool sequence_extent(const PageTable& t, int b, int& first, int& len) {
-  const int lo = __ldg(t.indptr + b), hi = __ldg(t.indptr + b + 1), last = __ldg(t.last_lens + b);
+  const int lo = t.indptr[b], hi = t.indptr[b + 1], last = t.last_lens[b];
   first = lo;
   len = 0;
   if (lo < 0 || hi < lo || hi > t.num_indices) {
@@ -50,7 +55,7 @@ __device__ __forceinline__ bool sequence_extent(const PageTable& t, int b, int& 
 // The page at entry `at` of the table (already known to be below num_indices); -1 and flagged
 // if it lies outside the buffer.
 __device__ __forceinline__ int table_page(const PageTable& t, int at) {
-  const int page = __ldg(t.indices + at);
+  const int page = t.indices[at];
   if (page < 0 || page >= t.num_pages) {
     raise_device_error(FP8MOE_DEVERR_PAGE);
     return -1;
@@ -122,10 +127,10 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
   const int ps = a.table.page_size;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the work before this in the stream is done
   const int count = count_sequences(
-      a.table.B, [&](int b) { return __ldg(a.append_indptr + b) / ps + 2ll * b <= blockIdx.x; });
+      a.table.B, [&](int b) { return a.append_indptr[b] / ps + 2ll * b <= blockIdx.x; });
   if (count == 0) return;
   const int b = count - 1;
-  const int lo = __ldg(a.append_indptr + b), hi = __ldg(a.append_indptr + b + 1);
+  const int lo = a.append_indptr[b], hi = a.append_indptr[b + 1];
   int first, len;
   const bool table = sequence_extent(a.table, b, first, len);
   const long long nth = blockIdx.x - (lo / ps + 2ll * b);    // negative only where the ranges decrease
@@ -152,7 +157,7 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
   };
 #pragma unroll
   for (int i = 0; i < kAppendHeld; ++i)
-    held[i] = active && r0 + i * side < rows ? __ldg(reinterpret_cast<const uint4*>(src + i * step)) : make_uint4(0, 0, 0, 0);
+    held[i] = active && r0 + i * side < rows ? *reinterpret_cast<const uint4*>(src + i * step) : make_uint4(0, 0, 0, 0);
   const int page = table_page(a.table, first + j);
   if (page < 0) return;                                      // (the same for the whole CTA)
   const float old = slot0 > 0 ? a.scale[page] : 0.0f;        // a page written from its first slot starts afresh
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
   for (int i = 0; i < kAppendHeld; ++i) take(held[i]);
   if (active)
     for (int r = r0 + kAppendHeld * side; r < rows; r += side)
-      take(__ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld)));
+      take(*reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld));
   mx = max(mx & 0xffffu, mx >> 16);
   mx = __reduce_max_sync(0xffffffffu, mx);
   if ((tid & 31) == 0) warp_max[tid >> 5] = mx;
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
     if (active && r0 + i * side < rows) store(i * side, held[i]);
   if (active)
     for (int r = r0 + kAppendHeld * side; r < rows; r += side)
-      store(r - r0, __ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld)));
+      store(r - r0, *reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld));
 
   if (slot0 > 0 && old > 0.0f && s > old) {                  // the rows that were there, in the larger scale
     const float ratio = old / s;
@@ -230,15 +235,15 @@ __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const Gat
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * kGatherRows;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the work before this in the stream is done
-  const int before = count_sequences(a.table.B, [&](int b) { return __ldg(a.out_indptr + b) <= t0; });
+  const int before = count_sequences(a.table.B, [&](int b) { return a.out_indptr[b] <= t0; });
   if (tid < kGatherRows) {
     const int t = t0 + tid;
     long long at = -1;
     float sc = 0.0f;
     int b = max(before - 1, 0);
-    while (b < a.table.B && __ldg(a.out_indptr + b + 1) <= t) ++b;
+    while (b < a.table.B && a.out_indptr[b + 1] <= t) ++b;
     if (t < a.T && b < a.table.B) {
-      const int lo = __ldg(a.out_indptr + b);
+      const int lo = a.out_indptr[b];
       int first, len;
       if (t >= lo && sequence_extent(a.table, b, first, len)) {
         const int i = t - lo;
@@ -248,7 +253,7 @@ __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const Gat
           const int page = table_page(a.table, first + i / a.table.page_size);
           if (page >= 0) {
             at = static_cast<long long>(page) * a.table.page_size + i % a.table.page_size;
-            sc = __ldg(a.scale + page);
+            sc = a.scale[page];
           }
         }
       }
@@ -257,14 +262,20 @@ __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const Gat
     row_scale[tid] = sc;
   }
   __syncthreads();
-  constexpr int kPieces = kLatDk / 16;
+  constexpr int kPieces = kLatDk / 16, kMine = (kGatherRows * kPieces + kGatherThreads - 1) / kGatherThreads;
+  uint4 codes[kMine];                                        // all loads before the first store
 #pragma unroll
-  for (int v = tid; v < kGatherRows * kPieces; v += kGatherThreads) {
-    const int r = v / kPieces, c = v - r * kPieces;
-    const long long at = row_at[r];
-    if (at < 0) continue;
+  for (int i = 0; i < kMine; ++i) {
+    const int v = tid + i * kGatherThreads, r = v / kPieces;
+    if (v < kGatherRows * kPieces && row_at[r] >= 0)
+      codes[i] = reinterpret_cast<const uint4*>(a.cache + row_at[r] * kLatDk)[v - r * kPieces];
+  }
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int v = tid + j * kGatherThreads, r = v / kPieces, c = v - r * kPieces;
+    if (v >= kGatherRows * kPieces || row_at[r] < 0) continue;
     const float s = row_scale[r];
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.cache + at * kLatDk) + c);
+    const uint4 x = codes[j];
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     __align__(16) __nv_bfloat162 y[8];
 #pragma unroll

@@ -819,3 +819,41 @@ def test_decode_of_an_empty_table():
         assert b.dt[1].numel() == 0
         o, lse = _decode(b, b.q(2, H))
         assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+# ---------------------------------------------------------------- calls that follow one another at once
+def test_each_call_sees_what_the_one_before_it_wrote():
+    """Steps in which every page's scale and codes change, run without a pause and with one after every
+    call: neighbouring pages' scales share memory lines that other SMs have read a call earlier."""
+    seqs, ps, H, steps = 96, 4, 16, 12
+    b = Batch([ps * 3] * seqs, ps, seed=90, poison=False).device()
+    rows = [(torch.randn(seqs, 576, generator=b.g) * 4.0 ** k).to(torch.bfloat16).to(DEV) for k in range(steps)]
+    q, ip = b.q(seqs, H, std=0.01).to(DEV), _indptr([1] * seqs).to(DEV)
+    tables = []
+    for k in range(steps):
+        counts = -(-(k + 1) // ps)
+        idx = b.dt[1].view(seqs, 3)[:, :counts].contiguous().view(-1)
+        tables.append((torch.arange(seqs + 1, dtype=torch.int32, device=DEV) * counts, idx,
+                       torch.full((seqs,), k + 1 - (counts - 1) * ps, dtype=torch.int32, device=DEV),
+                       torch.arange(seqs + 1, dtype=torch.int32, device=DEV) * (k + 1)))
+
+    def run(pause):
+        cache, scale, got = b.dc.clone(), b.ds.clone(), []
+        outs = [torch.empty(seqs * (k + 1), 576, dtype=torch.bfloat16, device=DEV) for k in range(steps)]
+        os_ = [torch.empty(seqs, H, 512, dtype=torch.bfloat16, device=DEV) for _ in range(steps)]
+        torch.cuda.synchronize()
+        for k, (indptr, idx, last, full) in enumerate(tables):
+            B.mla_kv_append_fp8(rows[k], ip, cache, scale, indptr, idx, last)
+            pause()
+            B.mla_kv_gather_fp8(cache, scale, indptr, idx, last, full, outs[k])
+            pause()
+            B.mla_decode_fp8_fwd(q, cache, scale, os_[k], indptr, idx, last)
+            pause()
+            got += [outs[k], os_[k]]
+        torch.cuda.synchronize()
+        return got + [scale, cache.view(torch.uint8)]
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        for x, y in zip(run(lambda: None), want):
+            assert torch.equal(x, y)

@@ -1,6 +1,8 @@
 """Host-side checks of the 8-bit latent cache's calls: what the library and the binding refuse
 before anything is launched."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -90,3 +92,14 @@ def test_binding_refuses_host_tensors():
                  lambda: B.mla_extend_fp8_fwd(q, i, cache, torch.zeros(2, 1), o, i, i, i[:1])):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+@pytest.mark.parametrize("file", ["mla_fp8_cache.cuh", "mla_fp8_attn.cuh"])
+def test_kernels_launched_early_do_not_read_through_the_read_only_path(file):
+    """They are resident while the work before them still writes what they read, so memory is not
+    read-only for as long as they live: no load may say that it is."""
+    with open(os.path.join(build.PKG_DIR, "csrc", file)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert "griddepcontrol.wait" in code
+    for words in ("__ldg", "ld.global.nc", "__ldlu", "ldg(", "__restrict__"):
+        assert words not in code, words
