@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
     for (int r = r0 + kAppendHeld * side; r < rows; r += side)
       store(r - r0, *reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld));
 
-  if (slot0 > 0 && old > 0.0f && s > old) {                  // the rows that were there, in the larger scale
+  // the rows that were there, in the larger scale (from a scale of 0, under which any code stands for 0, as codes of 0)
+  if (slot0 > 0 && s > old) {
     const float ratio = old / s;
     uint4* codes = reinterpret_cast<uint4*>(page_codes);
     for (long long v = tid; v < static_cast<long long>(slot0) * (kLatDk / 16); v += blockDim.x) {

@@ -65,7 +65,7 @@ def append(kv_new, append_indptr, codes, scales, kv_indptr, kv_indices, kv_last_
             slot = pos - j * ps
             old = float(scales[page, 0]) if slot > 0 else 0.0
             s = max(old, scale_of(rows))
-            if slot > 0 and 0.0 < old < s:
+            if slot > 0 and old < s:
                 before = e4m3_decode(codes[page, :slot, 0]).float() * (old / s)
                 codes[page, :slot, 0] = e4m3_encode(before)
             codes[page, slot:slot + rows.shape[0], 0] = e4m3_encode(rows * (1.0 / s) if s > 0 else rows)

@@ -857,3 +857,35 @@ def test_each_call_sees_what_the_one_before_it_wrote():
     for _ in range(5):
         for x, y in zip(run(lambda: None), want):
             assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------- pages whose scale was 0
+def test_append_after_a_row_of_infinities_and_zeros():
+    """The page's scale is 0 and its codes +-448: the value 0, which the next rows must not change."""
+    ps = 8
+    full = Batch([8], ps, seed=91, poison=False).device()
+    page = int(full.indices[0])
+
+    def step(have, x):
+        full.last = torch.tensor([have], dtype=torch.int32)
+        full.dt = tuple(t.to(DEV) for t in full.table)
+        _append_and_check(full, x.to(torch.bfloat16), [x.shape[0]])
+
+    x = torch.zeros(2, 576)
+    x[0, 0], x[0, 1], x[1, 2], x[1, 575] = math.inf, -math.inf, math.nan, math.inf
+    step(2, x)
+    assert float(full.ds[page]) == 0
+    step(3, torch.zeros(1, 576))                           # still nothing finite
+    step(4, torch.randn(1, 576, generator=full.g))
+    out = torch.full((4, 576), 9.0, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_gather_fp8(full.dc, full.ds, *full.dt, _indptr([4]).to(DEV), out)
+    got = out[:3].cpu().float()
+    assert torch.isnan(got[1, 2]) and (torch.nan_to_num(got) == 0).all() and torch.isnan(got).sum() == 1
+
+
+def test_append_to_a_callers_page_of_scale_zero():
+    """Any codes under a scale of 0 stand for 0."""
+    b = Batch([20, 9], 16, seed=92, poison=False)
+    b.scales[:] = 0.0
+    b.device()
+    _append_and_check(b, torch.randn(5, 576, generator=b.g).to(torch.bfloat16), [3, 2])

@@ -81,3 +81,17 @@ def test_queries_before_the_first_token_see_nothing_and_gather_rounds_once():
     assert o[1, 0, 0] == 0.5625 and lse[1, 0].item() == pytest.approx(576 * 0.5625 / 24)
     out = M8.gather(codes, scales, [0, 1], [0], [1, 3], torch.full((4, 576), 7.0, dtype=torch.bfloat16))
     assert (out[1:3] == 0.5625).all() and (out[0] == 7).all() and (out[3] == 7).all()
+
+
+def test_append_clears_codes_of_a_page_whose_scale_was_zero():
+    """A row of zeros and infinities has scale 0 and codes of +-448, which stand for 0; they still stand
+    for 0 (and NaN for NaN) once a later row raises the page's scale."""
+    ps, codes, scales = 4, torch.zeros(1, 4, 1, 576, dtype=torch.uint8), torch.zeros(1, 1)
+    x = torch.zeros(1, 576)
+    x[0, 0], x[0, 1], x[0, 2] = math.inf, -math.inf, math.nan
+    c, s = M8.append(x, [0, 1], codes, scales, *_table(1, ps, [0]))
+    assert s[0, 0] == 0 and e4m3_decode(c[0, 0, 0])[:2].tolist() == [448.0, -448.0]
+    c, s = M8.append(torch.full((1, 576), 1.75), [0, 1], c, s, *_table(2, ps, [0]))
+    assert s[0, 0] == 2.0 ** -8
+    v = e4m3_decode(c[0, :2, 0]) * 2.0 ** -8
+    assert (v[0, :2] == 0).all() and math.isnan(v[0, 2]) and (v[0, 3:] == 0).all() and (v[1] == 1.75).all()
