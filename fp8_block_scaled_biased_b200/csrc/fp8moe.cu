@@ -1244,8 +1244,9 @@ int mla_kv_gather_fp8(const uint8_t* kv_cache, const float* kv_scale, const int3
   a.ld = ld_out;
   a.T = num_rows;
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ld_out % 16 == 0;
-  return launch_early(name, mla_kv_gather_kernel, dim3((num_rows + kGatherRows - 1) / kGatherRows), kGatherThreads, 0,
-                      static_cast<cudaStream_t>(stream), a);
+  // 32 rows a CTA; and a thread for every range, which it checks
+  const unsigned ctas = std::max((num_rows + kGatherRows - 1) / kGatherRows, (batch + kGatherThreads - 1) / kGatherThreads);
+  return launch_early(name, mla_kv_gather_kernel, dim3(ctas), kGatherThreads, 0, static_cast<cudaStream_t>(stream), a);
 }
 
 // Workspace of the attention calls: the joining kernel's jobs, then the parts' references and

@@ -80,6 +80,9 @@ __device__ __forceinline__ float2 bf16x2_to_float(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
+// Whether a sequence's range lo .. hi - 1 lies within `rows` rows.
+__device__ __forceinline__ bool range_fits(int lo, int hi, int rows) { return lo >= 0 && hi >= lo && hi <= rows; }
+
 // ---------------------------------------------------------------- append
 struct AppendArgs {
   const __nv_bfloat16* kv_new;   // [T, 576], row stride ld
@@ -236,7 +239,14 @@ __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const Gat
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * kGatherRows;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the work before this in the stream is done
+  // Every range is looked at by some thread, the ones without a row here too (asked for before the search, as
+  // both wait for memory).
+  const int looked = blockIdx.x * kGatherThreads + tid;
+  int2 range = make_int2(0, 0);
+  if (looked < a.table.B) range = make_int2(a.out_indptr[looked], a.out_indptr[looked + 1]);
   const int before = count_sequences(a.table.B, [&](int b) { return a.out_indptr[b] <= t0; });
+  if (!range_fits(range.x, range.y, a.T)) raise_device_error(FP8MOE_DEVERR_PAGE);
+  if (t0 >= a.T) return;
   if (tid < kGatherRows) {
     const int t = t0 + tid;
     long long at = -1;
@@ -246,9 +256,9 @@ __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const Gat
     if (t < a.T && b < a.table.B) {
       const int lo = a.out_indptr[b];
       int first, len;
-      if (t >= lo && sequence_extent(a.table, b, first, len)) {
+      if (t >= lo && range_fits(lo, a.out_indptr[b + 1], a.T) && sequence_extent(a.table, b, first, len)) {
         const int i = t - lo;
-        if (lo < 0 || i >= len) {
+        if (i >= len) {
           raise_device_error(FP8MOE_DEVERR_PAGE);
         } else {
           const int page = table_page(a.table, first + i / a.table.page_size);

@@ -889,3 +889,88 @@ def test_append_to_a_callers_page_of_scale_zero():
     b.scales[:] = 0.0
     b.device()
     _append_and_check(b, torch.randn(5, 576, generator=b.g).to(torch.bfloat16), [3, 2])
+
+
+# ---------------------------------------------------------------- ranges, one call at a time
+def _gather_flagged(b, ip, rows, behind=0):
+    """One gather of `rows` rows with ranges that are wrong: flagged; returns what it left in the rows."""
+    out = torch.full((rows + behind, 576), 9.0, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, torch.tensor(ip, dtype=torch.int32, device=DEV), out[:rows])
+    assert B.device_status() == 32, ip
+    assert (out[rows:] == 9).all()
+    return out[:rows].cpu()
+
+
+def test_gather_ranges_out_of_bounds_are_flagged_and_their_rows_left():
+    b = Batch([20, 30, 40], 8, seed=93).device()
+    want = [M8.gather(b.codes, b.scales, b.indptr, b.indices, [0] * (s + 1) + [4] * (3 - s),
+                      torch.zeros(4, 576, dtype=torch.bfloat16)) for s in range(3)]
+    # the last range ends behind the output: its rows are left, the first one's written
+    got = _gather_flagged(b, [0, 1, 1, 3], 2, behind=4)
+    assert torch.equal(got[0], want[0][0]) and (got[1] == 9).all()
+    # it begins at or behind the end, so that no row belongs to it
+    got = _gather_flagged(b, [0, 0, 2, 5], 2, behind=4)
+    assert torch.equal(got, want[1][:2])
+    got = _gather_flagged(b, [0, 2, 7, 9], 2, behind=8)
+    assert torch.equal(got, want[0][:2])
+    # negative starts
+    assert (_gather_flagged(b, [0, -5, 2, 2], 2, behind=4) == 9).all()
+    got = _gather_flagged(b, [-2, 1, 2, 4], 4)
+    assert (got[0] == 9).all() and torch.equal(got[1:2], want[1][:1]) and torch.equal(got[2:], want[2][:2])
+    # ranges that decrease: rows claimed twice may be either's
+    got = _gather_flagged(b, [0, 3, 1, 4], 6)
+    assert (got[4:] == 9).all()
+    # all of them, far out
+    assert (_gather_flagged(b, [2 ** 31 - 1] * 4, 3, behind=4) == 9).all()
+    assert (_gather_flagged(b, [-2 ** 31, 0, 0, 0], 3, behind=4) == 9).all()
+
+
+def test_gather_a_bad_range_among_many_sequences():
+    """More sequences than one CTA's threads, few rows: the wrong range has none of them."""
+    n = 5000
+    b = Batch([1] * 3, 4, seed=94).device()
+    indptr = torch.full((n + 1,), 3, dtype=torch.int32)
+    indptr[:3] = torch.arange(3)
+    table = (indptr.to(DEV), b.dt[1], torch.cat([b.dt[2], torch.zeros(n - 3, dtype=torch.int32, device=DEV)]))
+    ip = indptr.clone()
+    out = torch.full((3, 576), 9.0, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_gather_fp8(b.dc, b.ds, *table, ip.to(DEV), out)
+    assert B.device_status() == 0
+    want = M8.gather(b.codes, b.scales, b.indptr, b.indices, [0, 1, 2, 3], torch.zeros(3, 576, dtype=torch.bfloat16))
+    assert torch.equal(out.cpu(), want)
+    for at, value in ((n, 4), (4000, 2), (300, 2 ** 31 - 1)):
+        bad = ip.clone()
+        bad[at] = value
+        out.fill_(9.0)
+        B.mla_kv_gather_fp8(b.dc, b.ds, *table, bad.to(DEV), out)
+        assert B.device_status() == 32, (at, value)
+
+
+def test_extend_ranges_out_of_bounds_are_flagged_and_their_rows_left():
+    b = Batch([20, 30], 8, seed=95, poison=False).device()
+    q = b.q(2, 16).to(DEV)
+    for bad, left in (([0, 1, 3], [1]), ([0, -5, 2], [0, 1]), ([-2, 1, 2], [0]), ([0, 2, 5], []), ([0, 2, 1], [])):
+        o = torch.full((2, 16, 512), 4.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((2, 16), 4.0, device=DEV)
+        B.mla_extend_fp8_fwd(q, torch.tensor(bad, dtype=torch.int32, device=DEV), b.dc, b.ds, o, *b.dt, lse=lse)
+        assert B.device_status() == 32, bad
+        for r in range(2):
+            assert (o[r] == 4).all() == (r in left) and (lse[r] == 4).all() == (r in left), (bad, r)
+
+
+def test_append_ranges_out_of_bounds_are_flagged_and_their_pages_left():
+    b = Batch([20, 30], 8, seed=96, poison=False).device()
+    before, scales = _codes(b.dc), b.ds.cpu()
+    x = torch.ones(2, 576, dtype=torch.bfloat16, device=DEV)
+    last = [int(b.indices[2]), int(b.indices[-1])]         # the page that each sequence's last token lies in
+    for bad, left in (([0, 1, 3], [1]), ([0, -5, 2], [0, 1]), ([-2, 1, 2], [0]), ([0, 2, 5], [1]), ([0, 1, 0], [1])):
+        b.device()
+        B.mla_kv_append_fp8(x, torch.tensor(bad, dtype=torch.int32, device=DEV), b.dc, b.ds, *b.dt)
+        assert B.device_status() == 32, bad
+        got, now = _codes(b.dc), b.ds.cpu()
+        mine = torch.zeros(len(scales), dtype=torch.bool)
+        for s in (0, 1):
+            if s not in left:
+                mine[last[s]] = True
+                assert not torch.equal(got[last[s]], before[last[s]])
+        assert torch.equal(got[~mine], before[~mine]) and torch.equal(now[~mine], scales[~mine]), bad
