@@ -129,15 +129,21 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
   const int tid = threadIdx.x;
   const int ps = a.table.page_size;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the work before this in the stream is done
+  // Every range is looked at by some thread (there are at least twice as many blocks as sequences): one that
+  // decreases may have no block, the next sequence's having taken its place.
+  const long long looked = static_cast<long long>(blockIdx.x) * blockDim.x + tid;
+  int2 range = make_int2(0, 0);
+  if (looked < a.table.B) range = make_int2(a.append_indptr[looked], a.append_indptr[looked + 1]);
   const int count = count_sequences(
       a.table.B, [&](int b) { return a.append_indptr[b] / ps + 2ll * b <= blockIdx.x; });
+  if (!range_fits(range.x, range.y, a.T)) raise_device_error(FP8MOE_DEVERR_PAGE);
   if (count == 0) return;
   const int b = count - 1;
   const int lo = a.append_indptr[b], hi = a.append_indptr[b + 1];
   int first, len;
   const bool table = sequence_extent(a.table, b, first, len);
   const long long nth = blockIdx.x - (lo / ps + 2ll * b);    // negative only where the ranges decrease
-  if (lo < 0 || hi < lo || hi > a.T || nth < 0 || (table && hi - lo > len)) {
+  if (!range_fits(lo, hi, a.T) || nth < 0 || (table && hi - lo > len)) {
     if (tid == 0) raise_device_error(FP8MOE_DEVERR_PAGE);
     return;
   }

@@ -974,3 +974,18 @@ def test_append_ranges_out_of_bounds_are_flagged_and_their_pages_left():
                 mine[last[s]] = True
                 assert not torch.equal(got[last[s]], before[last[s]])
         assert torch.equal(got[~mine], before[~mine]) and torch.equal(now[~mine], scales[~mine]), bad
+
+
+@pytest.mark.parametrize("ranges, rows, ps", [
+    ([5, 3, 5], 7, 1), ([0, 2, 0, 2, 2], 2, 1), ([1, 2, 0, 0], 2, 1), ([10, 7, 10], 20, 2), ([16, 19, 14, 17, 20], 25, 2),
+    ([9, 0, 4, 4], 13, 4), ([0, 0, 40, 40, 4, 5], 60, 4), ([0, 60, 0, 60, 0, 60], 60, 1), ([0, 9, 9, 9, -1, 9], 60, 1)])
+def test_append_every_range_that_decreases_is_flagged(ranges, rows, ps):
+    """One that decreases by several pages has no block of its own: the next sequence's begin first."""
+    b = Batch([60] * (len(ranges) - 1), ps, seed=97, poison=False).device()
+    x = torch.ones(rows, 576, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_append_fp8(x, torch.tensor(ranges, dtype=torch.int32, device=DEV), b.dc, b.ds, *b.dt)
+    assert B.device_status() == 32
+    b.device()
+    ranges = sorted(max(0, r) for r in ranges)
+    B.mla_kv_append_fp8(x, torch.tensor(ranges, dtype=torch.int32, device=DEV), b.dc, b.ds, *b.dt)
+    assert B.device_status() == 0
