@@ -685,7 +685,8 @@ int mla_kv_gather_fp8(const uint8_t* kv_cache, const float* kv_scale,
  * largest magnitude: to 2^-21 of that). The softmax weights that multiply the values are
  * rounded to the sum of three e4m3 codes, off by at most 2^-12 of themselves or 2^-22 of the
  * largest weight times scale (2^-24 in contexts above 2^14 tokens, 2^-26 above 2^16); the sum
- * that divides them, and lse, are not rounded. An infinite query entry counts as NaN. A NaN
+ * that divides them, and lse, are not rounded. The soft cap, of any size, is off by at most
+ * 2^-19 of the score it caps. An infinite query entry counts as NaN. A NaN
  * in a cached row reaches every query that sees the row, and no other.
  */
 size_t mla_fp8_workspace(int num_heads, int num_q);

@@ -989,3 +989,23 @@ def test_append_every_range_that_decreases_is_flagged(ranges, rows, ps):
     ranges = sorted(max(0, r) for r in ranges)
     B.mla_kv_append_fp8(x, torch.tensor(ranges, dtype=torch.int32, device=DEV), b.dc, b.ds, *b.dt)
     assert B.device_status() == 0
+
+
+# ---------------------------------------------------------------- soft caps of any size
+# Capping a score t is off by less than 2^-19.5 of it: below half the cap by a few 2^-24. Above, with x = t / cap,
+# u = 1 / (1 + e^2x) is relatively off by 2^-22 + 2^-24 (quotient, sum) and by 1 - u times e^2x's 2^-22 +
+# 3 * 2^-24: 1 - 2 u by 2.6 * 2^-22 at most, where it is 0.46 or more. Together with the 18 * 2^-23 = 2^-18.8 S
+# of the scores' sums that is still below 2^-18 S.
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 0.5, 50.0, 1e4, 1e6, 1e8, 1e30, 3e38])
+@pytest.mark.parametrize("H, ps", [(16, 64), (40, 3)])
+def test_soft_cap_keeps_the_scores_precision(cap, H, ps):
+    b = Batch([40, 300, 77, 1], ps, seed=98).device(wide=H > 16)
+    cap = float(torch.tensor(cap, dtype=torch.float32))    # the call takes it in 32 bits
+    for std, sm_scale in ((6.0, 0.11), (1.0, None), (1e-3, None)):
+        q = b.q(4, H, std=std)
+        o, lse = _decode(b, q, logit_cap=cap, sm_scale=sm_scale)
+        _check(b, q, torch.arange(5), o, lse, logit_cap=cap, sm_scale=sm_scale)
+    q = b.q(4, H, std=6.0)
+    q[1] = 0.0
+    o, lse = _extend(b, q, _indptr([0, 3, 1, 0]), logit_cap=cap)
+    _check(b, q, _indptr([0, 3, 1, 0]), o, lse, logit_cap=cap)
