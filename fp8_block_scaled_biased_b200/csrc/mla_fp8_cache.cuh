@@ -83,6 +83,15 @@ __device__ __forceinline__ float2 bf16x2_to_float(uint32_t v) {
 // Whether a sequence's range lo .. hi - 1 lies within `rows` rows.
 __device__ __forceinline__ bool range_fits(int lo, int hi, int rows) { return lo >= 0 && hi >= lo && hi <= rows; }
 
+// A product with a caller's scale that is no power of two. fp32 would round it before the bf16 value does, now and
+// then onto the middle of two of those; here the neighbour with an odd last bit stands for what lies between two
+// fp32 values, so that the later rounding is as good as the only one.
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
+__device__ __forceinline__ float odd_of(float down, float up) {
+  return down == up || (__float_as_uint(down) & 1u) ? down : up;
+}
+__device__ __forceinline__ float product_to_odd(float x, float s) { return odd_of(__fmul_rd(x, s), __fmul_ru(x, s)); }
+
 // ---------------------------------------------------------------- append
 struct AppendArgs {
   const __nv_bfloat16* kv_new;   // [T, 576], row stride ld
@@ -237,6 +246,22 @@ struct GatherArgs {
 constexpr int kGatherRows = 32;
 constexpr int kGatherThreads = 256;
 
+// 16 codes under a scale that is no power of two (out of line: in the loop below it cost short prefixes 0.5 us).
+__device__ __noinline__ void gather_under_any_scale(const uint4 codes, float s, __nv_bfloat16* dst) {
+  uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i, dst += 4) {
+    const float4 f = e4m3x4_to_float(w[0]);
+    w[0] = w[1];
+    w[1] = w[2];
+    w[2] = w[3];
+    dst[0] = __float2bfloat16_rn(product_to_odd(f.x, s));
+    dst[1] = __float2bfloat16_rn(product_to_odd(f.y, s));
+    dst[2] = __float2bfloat16_rn(product_to_odd(f.z, s));
+    dst[3] = __float2bfloat16_rn(product_to_odd(f.w, s));
+  }
+}
+
 // A CTA reads back 32 output rows: their cache rows first (a thread each), then 16 codes at a
 // time (one 16-byte load, one 32-byte store). Bound by HBM, of whose bytes two thirds are written.
 __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const GatherArgs a) {
@@ -302,7 +327,9 @@ __global__ void __launch_bounds__(kGatherThreads) mla_kv_gather_kernel(const Gat
       y[2 * i + 1] = __floats2bfloat162_rn(f.z * s, f.w * s);
     }
     uint4* dst = reinterpret_cast<uint4*>(a.out + (t0 + r) * a.ld) + 2 * c;
-    if (a.wide) {
+    if (!power_of_two(s)) {
+      gather_under_any_scale(x, s, reinterpret_cast<__nv_bfloat16*>(dst));
+    } else if (a.wide) {
       st_global_v8(dst, reinterpret_cast<const uint32_t(&)[8]>(y));
     } else {
       dst[0] = *reinterpret_cast<const uint4*>(&y[0]);

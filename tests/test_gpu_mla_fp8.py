@@ -1009,3 +1009,26 @@ def test_soft_cap_keeps_the_scores_precision(cap, H, ps):
     q[1] = 0.0
     o, lse = _extend(b, q, _indptr([0, 3, 1, 0]), logit_cap=cap)
     _check(b, q, _indptr([0, 3, 1, 0]), o, lse, logit_cap=cap)
+
+
+# ---------------------------------------------------------------- a caller's scales: no powers of two
+def _single_token_batch(scales, seed, slots=1):
+    """A sequence per scale, a page each of `slots` + 1 slots, one of them still free."""
+    n = len(scales)
+    b = Batch([slots + 1] * n, slots + 1, seed=seed, spare=0, poison=False)
+    b.scales[b.indices.long(), 0] = torch.tensor(scales, dtype=torch.float32)
+    return b
+
+
+def test_gather_rounds_once_under_any_scale():
+    """Products next to the middle of two bf16 values, which fp32 would round to the middle: tie / c with a
+    last bit, times c; beside arbitrary scales, and ones below fp32's normal range."""
+    scales = [t / c for c in (9, 11, 13, 15) for t in range(257, 512, 2)] + [1.37e-3, 3.1e5, 1e-38, 3e-39, 1e-44, 2.0 ** -130, 0.0,
+                                                                             3e38, 1.5 * 2.0 ** 119]
+    b = _single_token_batch(scales, 100)
+    b.device()
+    ip = _indptr(b.lens)
+    out = torch.zeros(sum(b.lens), 576, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, ip.to(DEV), out)
+    want = M8.gather(b.codes, b.scales, b.indptr, b.indices, ip, torch.zeros_like(out).cpu())
+    assert torch.equal(out.cpu().view(torch.int16), want.view(torch.int16))
