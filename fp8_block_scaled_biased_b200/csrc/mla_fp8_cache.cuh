@@ -83,14 +83,15 @@ __device__ __forceinline__ float2 bf16x2_to_float(uint32_t v) {
 // Whether a sequence's range lo .. hi - 1 lies within `rows` rows.
 __device__ __forceinline__ bool range_fits(int lo, int hi, int rows) { return lo >= 0 && hi >= lo && hi <= rows; }
 
-// A product with a caller's scale that is no power of two. fp32 would round it before the bf16 value does, now and
-// then onto the middle of two of those; here the neighbour with an odd last bit stands for what lies between two
-// fp32 values, so that the later rounding is as good as the only one.
+// Products and quotients under a caller's scale that is no power of two. fp32 would round them before the code
+// or bf16 value does, now and then onto the middle of two of those; here the neighbour with an odd last
+// bit stands for what lies between two fp32 values, so that the later rounding is as good as the only one.
 __device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
 __device__ __forceinline__ float odd_of(float down, float up) {
   return down == up || (__float_as_uint(down) & 1u) ? down : up;
 }
 __device__ __forceinline__ float product_to_odd(float x, float s) { return odd_of(__fmul_rd(x, s), __fmul_ru(x, s)); }
+__device__ __forceinline__ float quotient_to_odd(float x, float s) { return odd_of(__fdiv_rd(x, s), __fdiv_ru(x, s)); }
 
 // ---------------------------------------------------------------- append
 struct AppendArgs {
@@ -125,6 +126,18 @@ __device__ __forceinline__ int count_sequences(int B, F&& starts_by) {
     hi = min(hi, lo + step - 1);
   }
   return hi;
+}
+
+// A thread's 8 columns of every `side`-th of `rows` rows, under a scale that is no power of two.
+__device__ __noinline__ void append_under_any_scale(const __nv_bfloat16* src, long long ld, uint8_t* dst, int rows, int side,
+                                                    float s) {
+  for (int r = 0; r < rows; r += side) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const float x = __bfloat162float(src[r * ld + i]);
+      dst[static_cast<size_t>(r) * kLatDk + i] = static_cast<uint8_t>(cvt_e4m3x2(quotient_to_odd(x, s), 0.0f));
+    }
+  }
 }
 
 // One CTA per (sequence, page written): the largest magnitude of the page's new rows, the page's
@@ -207,12 +220,16 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
         make_uint2(float_to_e4m3x4(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv),
                    float_to_e4m3x4(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv));
   };
+  if (power_of_two(s)) {
 #pragma unroll
-  for (int i = 0; i < kAppendHeld; ++i)
-    if (active && r0 + i * side < rows) store(i * side, held[i]);
-  if (active)
-    for (int r = r0 + kAppendHeld * side; r < rows; r += side)
-      store(r - r0, *reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld));
+    for (int i = 0; i < kAppendHeld; ++i)
+      if (active && r0 + i * side < rows) store(i * side, held[i]);
+    if (active)
+      for (int r = r0 + kAppendHeld * side; r < rows; r += side)
+        store(r - r0, *reinterpret_cast<const uint4*>(src + static_cast<long long>(r - r0) * a.ld));
+  } else if (active) {
+    append_under_any_scale(src, a.ld, dst, rows - r0, side, s);
+  }
 
   // the rows that were there, in the larger scale (from a scale of 0, under which any code stands for 0, as codes of 0)
   if (slot0 > 0 && s > old) {
@@ -224,7 +241,9 @@ __global__ void __launch_bounds__(512, 2) mla_kv_append_kernel(const AppendArgs 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float4 f = e4m3x4_to_float(w[i]);
-        w[i] = float_to_e4m3x4(f.x * ratio, f.y * ratio, f.z * ratio, f.w * ratio);
+        w[i] = power_of_two(old) ? float_to_e4m3x4(f.x * ratio, f.y * ratio, f.z * ratio, f.w * ratio)
+                                 : float_to_e4m3x4(product_to_odd(f.x, ratio), product_to_odd(f.y, ratio),
+                                                   product_to_odd(f.z, ratio), product_to_odd(f.w, ratio));
       }
       codes[v] = x;
     }

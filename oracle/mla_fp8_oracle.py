@@ -41,6 +41,13 @@ def scale_of(x: torch.Tensor) -> float:
     return 2.0 ** e
 
 
+def codes_of(x: torch.Tensor) -> torch.Tensor:
+    """The nearest codes of the fp64 values x, ties to even, saturating; NaN stays NaN."""
+    finite = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+    step = torch.exp2((torch.frexp(finite)[1] - 1).clamp(min=-6).to(F64) - 3)
+    return e4m3_encode(torch.where(torch.isfinite(x), torch.round(finite / step) * step, x))
+
+
 def lengths(kv_indptr, kv_last_page_lens, page_size: int) -> list[int]:
     out = []
     for b in range(len(kv_last_page_lens)):
@@ -66,9 +73,8 @@ def append(kv_new, append_indptr, codes, scales, kv_indptr, kv_indices, kv_last_
             old = float(scales[page, 0]) if slot > 0 else 0.0
             s = max(old, scale_of(rows))
             if slot > 0 and old < s:
-                before = e4m3_decode(codes[page, :slot, 0]).float() * (old / s)
-                codes[page, :slot, 0] = e4m3_encode(before)
-            codes[page, slot:slot + rows.shape[0], 0] = e4m3_encode(rows * (1.0 / s) if s > 0 else rows)
+                codes[page, :slot, 0] = codes_of(e4m3_decode(codes[page, :slot, 0]).to(F64) * old / s)
+            codes[page, slot:slot + rows.shape[0], 0] = codes_of(rows.to(F64) / s if s > 0 else rows.to(F64))
             scales[page, 0] = s
             pos = end
     return codes, scales

@@ -1032,3 +1032,24 @@ def test_gather_rounds_once_under_any_scale():
     B.mla_kv_gather_fp8(b.dc, b.ds, *b.dt, ip.to(DEV), out)
     want = M8.gather(b.codes, b.scales, b.indptr, b.indices, ip, torch.zeros_like(out).cpu())
     assert torch.equal(out.cpu().view(torch.int16), want.view(torch.int16))
+
+
+def test_append_rounds_once_into_pages_of_any_scale():
+    """New rows x / scale next to the middle of two codes, into pages whose scale stays: 7 (ties themselves), and
+    x / tie with a last bit; then codes times old / scale next to it, into pages whose scale grows."""
+    g = torch.Generator().manual_seed(101)
+    # (quotients stay below 31 / 16 * 2^6: twice that is below 448, so no scale grows)
+    pairs = [(float(x), x * 16 / t) for x in range(128, 256, 3) for t in range(17, 32, 2)] + [(10.9375, 7.0), (12.6875, 7.0)]
+    b = _single_token_batch([s for _, s in pairs], 101).device()
+    x = torch.tensor([[x] for x, _ in pairs]) * torch.exp2(torch.randint(-8, 7, (len(pairs), 576), generator=g).float())
+    x[:, ::2] *= -1
+    x[:, 1], x[:, 3], x[:, 5] = math.inf, math.nan, 0.0
+    before = b.scales.clone()
+    _append_and_check(b, x.to(torch.bfloat16), [1] * len(pairs))
+    assert torch.equal(b.scales, before)
+    pairs = [(c, t) for c in (9, 11, 13, 15) for t in range(17, 32, 2)]
+    b = _single_token_batch([t / c for c, t in pairs], 102, slots=5).device()
+    x = torch.randn(len(pairs), 576, generator=g)
+    x[:, 7] = 448.0 * 3
+    _append_and_check(b, x.to(torch.bfloat16), [1] * len(pairs))
+    assert (b.scales == 4).all()

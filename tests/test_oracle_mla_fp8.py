@@ -1,5 +1,6 @@
 """Pins for the 8-bit latent cache's oracle: cases by hand and against other definitions."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -95,3 +96,29 @@ def test_append_clears_codes_of_a_page_whose_scale_was_zero():
     assert s[0, 0] == 2.0 ** -8
     v = e4m3_decode(c[0, :2, 0]) * 2.0 ** -8
     assert (v[0, :2] == 0).all() and math.isnan(v[0, 2]) and (v[0, 3:] == 0).all() and (v[1] == 1.75).all()
+
+
+def test_append_rounds_once_where_a_page_came_with_a_scale_that_is_no_power_of_two():
+    """Quotients at or next to the middle of two codes, which a rounding before the code's would move there."""
+    ps = 2
+
+    def nearest(q, step):                                          # of the fraction q, ties to even
+        n = q / step
+        lo = n.numerator // n.denominator
+        up = n - lo > Fraction(1, 2) or (n - lo == Fraction(1, 2) and lo % 2)
+        return float((lo + up) * step)
+
+    for x, old in ((10.9375, 7.0), (12.6875, 7.0), (128.0, 128 * 16 / 19), (128.0, 128 * 16 / 29), (129.0, 129 * 16 / 21)):
+        scale = torch.tensor([[old]], dtype=torch.float32)
+        q = Fraction(x) / Fraction(scale.item())
+        assert 1 < q < 2 and abs(q * 16 - round(q * 16)) < Fraction(1, 2 ** 18) and round(q * 16) % 2
+        c, s = M8.append(torch.full((1, 576), x), [0, 1], torch.zeros(1, 2, 1, 576, dtype=torch.uint8), scale,
+                         *_table(2, ps, [0]))
+        assert s[0, 0] == scale[0, 0] and (e4m3_decode(c[0, 1, 0]) == nearest(q, Fraction(1, 8))).all()
+    # and codes carried over to a larger scale
+    for code, tie in ((9, 29), (9, 31), (11, 23), (13, 19), (15, 31)):
+        scale = torch.tensor([[tie / code]], dtype=torch.float32)
+        q = code * Fraction(scale.item()) / 4
+        c, s = M8.append(torch.full((1, 576), 1000.0), [0, 1], e4m3_encode(torch.full((1, 2, 1, 576), float(code))), scale,
+                         *_table(2, ps, [0]))
+        assert s[0, 0] == 4.0 and q * 4 != tie and (e4m3_decode(c[0, 0, 0]) == nearest(q, Fraction(1, 2))).all()
