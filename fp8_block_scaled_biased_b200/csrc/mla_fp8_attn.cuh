@@ -240,17 +240,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two fp16 -> two e4m3 codes, and back.
-__device__ __forceinline__ uint16_t half2_to_e4m3x2(__half2 v) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
-  return r;
-}
-__device__ __forceinline__ __half2 e4m3x2_to_half2(uint16_t v) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
-  return *reinterpret_cast<const __half2*>(&r);
-}
 
 // ---------------------------------------------------------------- work list
 // A sequence's share of the work list; one with no query or a bad table has none.
