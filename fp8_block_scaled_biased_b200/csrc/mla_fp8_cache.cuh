@@ -114,7 +114,7 @@ __device__ __forceinline__ uint32_t finite_magnitudes(uint32_t v) {
 }
 
 // Sequences that start by some place, which grows with b: all threads of the CTA search together, one
-// round where there are no more sequences than threads, two or three for the most there can be.
+// round where there are no more sequences than threads, three (256 threads) or four (96) for the 2^20 there can be.
 template <typename F>
 __device__ __forceinline__ int count_sequences(int B, F&& starts_by) {
   const int threads = static_cast<int>(blockDim.x);

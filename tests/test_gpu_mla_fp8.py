@@ -1053,3 +1053,73 @@ def test_append_rounds_once_into_pages_of_any_scale():
     x[:, 7] = 448.0 * 3
     _append_and_check(b, x.to(torch.bfloat16), [1] * len(pairs))
     assert (b.scales == 4).all()
+
+
+# ---------------------------------------------------------------- whole sequences, bad tables call by call
+@pytest.mark.parametrize("many", [1, 100, 148])
+def test_decode_whole_sequences_of_the_smallest_scale(many):
+    """Up to as many sequences as CTAs, all of 13 tiles: each is taken whole by one CTA (alone it is cut).
+    Their scores rise after the first tile by just less than what moves a reference, under the
+    smallest scale that an append writes: the sum of 1472 weights stays finite in one place. Any output is
+    a mean of values, so it is off by at most twice the largest, 448 * 2^-110."""
+    b = Batch([1600], 64, seed=15, scale_exp=(-110, -110))
+    flat = b.codes.view(-1, 576)
+    at = b.indices[torch.arange(1600) // 64].long() * 64 + torch.arange(1600) % 64
+    flat[at, 575] = e4m3_encode(torch.where(torch.arange(1600) >= 128, 128.0, 0.0))
+    b.device()
+    q = torch.zeros(1, 16, 576)
+    q[:, :, 575] = 2.0 ** 103 * 5.75 * math.log(2.0)
+    q = q.to(torch.bfloat16)
+    ref, ref_lse, _, size, _ = M8.decode(q, b.codes, b.scales, *b.table, sm_scale=1.0)
+    b.dt = (torch.arange(many + 1, dtype=torch.int32, device=DEV) * 25, b.dt[1].repeat(many), b.dt[2].repeat(many))
+    o, lse = _decode(b, q.expand(many, 16, 576).contiguous(), sm_scale=1.0)
+    dl = (lse.cpu().double() - ref_lse).abs()
+    assert (dl <= 2.0 ** -17 * (1 + size) + 2.0 ** -21 * (1 + ref_lse.abs())).all()
+    assert ((o.cpu().double() - ref).abs() <= 2 * 448 * 2.0 ** -110).all()
+
+
+@pytest.mark.parametrize("kind", ["page below", "page above", "table end", "table start", "last 0", "last above"])
+def test_a_bad_table_leaves_the_other_sequences_right(kind):
+    """One sequence's entries are out of range: each call flags it, the others' results are right, and rows and
+    pages that are not the bad sequence's stay as they were."""
+    lens = [20, 30, 17]
+    b = Batch(lens, 8, seed=103, poison=False).device()
+    indptr, indices, last = (t.clone() for t in b.table)
+    if kind.startswith("page"):
+        indices[2] = -1 if kind == "page below" else b.codes.shape[0]       # the first sequence's last page
+    elif kind == "table end":                              # the last sequence's pages pass the table's end
+        indptr[3] = indices.numel() + 1
+    elif kind == "table start":
+        indptr[0] = -1
+    else:
+        last[0] = 0 if kind == "last 0" else 9
+    bad = 2 if kind == "table end" else 0
+    fine = [s for s in range(3) if s != bad]
+    table = tuple(t.to(DEV) for t in (indptr, indices, last))
+    ip, full = _indptr([1, 1, 1]), _indptr(lens)
+    q = b.q(3, 16)
+    ref, ref_lse, mag, size, coded = M8.decode(q, b.codes, b.scales, *b.table)
+    bound = _bound(ref, mag, size, coded, 30)
+    for qo in (None, ip.to(DEV)):
+        o = torch.full((3, 16, 512), 4.0, dtype=torch.bfloat16, device=DEV)
+        if qo is None:
+            B.mla_decode_fp8_fwd(q.to(DEV), b.dc, b.ds, o, *table)
+        else:
+            B.mla_extend_fp8_fwd(q.to(DEV), qo, b.dc, b.ds, o, *table)
+        assert B.device_status() == 32
+        assert ((o.cpu().double() - ref).abs()[fine] <= bound[fine]).all()
+    out = torch.full((sum(lens) + 3, 576), 4.0, dtype=torch.bfloat16, device=DEV)
+    B.mla_kv_gather_fp8(b.dc, b.ds, *table, full.to(DEV), out)
+    assert B.device_status() == 32
+    want = M8.gather(b.codes, b.scales, b.indptr, b.indices, full, torch.full((sum(lens) + 3, 576), 4.0, dtype=torch.bfloat16))
+    for s in fine:
+        assert torch.equal(out[full[s]:full[s + 1]].cpu(), want[full[s]:full[s + 1]])
+    assert (out[sum(lens):] == 4).all()
+    x = torch.randn(3, 576, generator=b.g).to(torch.bfloat16)
+    want_c, want_s = M8.append(x, ip, b.codes, b.scales, *b.table)
+    B.mla_kv_append_fp8(x.to(DEV), ip.to(DEV), b.dc, b.ds, *table)
+    assert B.device_status() == 32
+    own = b.indices[b.indptr[bad]:b.indptr[bad + 1]].long()
+    other = torch.ones(b.codes.shape[0], dtype=torch.bool)
+    other[own] = False
+    assert torch.equal(_codes(b.dc)[other], want_c[other]) and torch.equal(b.ds.cpu()[other], want_s[other])
