@@ -1141,8 +1141,8 @@ int mla_decode_fwd(const uint16_t* q, const uint16_t* kv_buffer, uint16_t* o, co
 namespace {
 
 // Launches a kernel while the work before it in the stream may still run (programmatic dependence): the
-// kernel waits for that work's end itself, once it is set up (64 x 544 tokens: 17.3 to 16.9 us; one
-// sequence of 97: 9.6 to 8.9; one new token for 64 sequences appended: 3.0 to 2.8).
+// kernel waits for that work's end itself, once it is set up (64 x 544 tokens: 17.4 to 17.1 us; one
+// sequence of 97: 10.0 to 9.2; one new token for 64 sequences appended: 3.0 to 2.8).
 template <typename... P, typename... A>
 int launch_early(const char* name, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A&&... args) {
   cudaLaunchAttribute attr[1];
@@ -1333,7 +1333,10 @@ static int mla_fp8_attention(const char* name, const uint16_t* q, const int32_t*
   // and the change of fragments (shorter with 16): below 7.5 tiles of 16 columns per SM. At 4.1 tiles (64 x
   // 600 tokens, two queries on 16 heads) 19.5 us with 16, 23.6 with 32; at 6.8 (64 x 1000, 32 heads) 24.6
   // and 29.2; at 8.1 (64 x 600, four queries) 30.2 and 24.6; at 8.9 (30 x 700, 128 heads) 30.7 and 25.1; at 41
-  // (24 x 4096, 128 heads, a page per token) 78 and 61. A gang of CTAs for a sequence's column groups.
+  // (24 x 4096, 128 heads, a page per token) 78 and 61. The table's length stands for the batch's pages, which the
+  // host does not know: with room to spare a short list counts as a long one (64 x 2 queries on 16 heads: 16.2 us
+  // with an exact table, 20.9 with room for 144K tokens more). A gang of CTAs for a sequence's column groups, by the
+  // average too.
   const long long cols = (static_cast<long long>(num_q) * num_heads + batch - 1) / batch;
   const long long tiles = (static_cast<long long>(num_indices) * page_size + kLatTile - 1) / kLatTile * ((cols + 15) / 16);
   const int hg = cols <= 16 || 2 * tiles < 15ll * sms ? 16 : 32;

@@ -624,16 +624,18 @@ int mla_decode_fwd(const uint16_t* q, const uint16_t* kv_buffer, uint16_t* o,
  *   kv_scale     fp32 [num_pages, 1]: value = code * scale, one scale per block of tokens
  *                (a page) and KV head. mla_kv_append_fp8 writes powers of two: the smallest
  *                s >= 2^-110 with amax <= 448 s, amax over the page's finite entries, 0 for
- *                a page whose finite entries are all zero. The attention and gather calls
- *                take any finite scale >= 0; the softmax weights keep the precision stated
- *                below for scales of 0 and from 2^-90 to 2^100.
+ *                a page whose finite entries are all zero, but keeps a larger one that a
+ *                page came with. All calls take any finite scale >= 0; the softmax weights
+ *                keep the precision stated below for scales of 0 and from 2^-90 to 2^100.
  *   kv_indptr, kv_indices, kv_last_page_lens: the page table, as for mla_decode_fwd.
  *                Sequence b holds L_b = (pages - 1) * page_size + kv_last_page_lens[b] tokens
  *                (0 without a page). Any page_size >= 1.
  * Limits of all four calls: batch <= 2^20; num_pages * page_size below 2^31, num_indices *
  * page_size up to 2^31 - 256. A page-table entry, or an append, query or output range, that is
  * out of range is neither read nor written through: the device error word gets
- * FP8MOE_DEVERR_PAGE and that sequence's output is unspecified. All are deterministic.
+ * FP8MOE_DEVERR_PAGE and that sequence's output is unspecified. Every range of a call is
+ * checked; a call without a row to work on (num_tokens, num_rows or num_q 0) launches nothing
+ * and checks none. All are deterministic.
  */
 
 /*
@@ -645,7 +647,8 @@ int mla_decode_fwd(const uint16_t* q, const uint16_t* kv_buffer, uint16_t* o,
  * For every page written: old = its scale, or 0 if its first slot is written now (a page
  * taken over from an earlier owner starts afresh); scale = max(old, the scale of the new
  * rows); if that exceeds old, the rows the page already held get the codes
- * e4m3(code * old / scale); new rows get e4m3(x / scale). Rounding is to nearest even;
+ * e4m3(code * old / scale) (0 for old = 0); new rows get e4m3(x / scale), or e4m3(x) where the
+ * scale is 0. Each is rounded once, to nearest even, whatever the scale;
  * infinities become +-448, NaN stays NaN. Rows of a page behind the last token, and pages
  * that no new token falls into, are left as they are.
  * A page must not be written for two sequences in one call, nor read by work that is not
@@ -660,7 +663,7 @@ int mla_kv_append_fp8(const uint16_t* kv_new, int ld_new, const int32_t* append_
 /*
  * Reads tokens back in bf16 (a cached prefix for the up-projection of a prompt's keys and
  * values): out[out_indptr[b] + i] = bf16(code * scale) of token i of sequence b, for the
- * first out_indptr[b + 1] - out_indptr[b] tokens (at most L_b) of each.
+ * first out_indptr[b + 1] - out_indptr[b] tokens (at most L_b) of each, rounded once.
  *   out_indptr  int32 [batch + 1], non-decreasing within [0, num_rows]
  *   out         bf16 [num_rows, 576], row stride ld_out (a multiple of 8), 16-byte aligned;
  *               rows outside the ranges are left as they are
